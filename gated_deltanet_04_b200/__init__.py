@@ -11,6 +11,8 @@ Entry points (same names as the C ABI):
     gdn_prefill(q, k, v, g, beta, initial_state=None, cu_seqlens=None, ...)
     gdn_decode_step(q, k, v, g, beta, state, ...)
     gdn_decode_step_bf16_state(q, k, v, g, beta, state, ...)
+    gdn_linear_*(q, k, v, log_decay, ...)   linear attention with a decay per head (linear.py)
+    gdn_qk_norm_rope(xq, xk, ...)           query/key norm with rotation (rope.py)
 """
 from __future__ import annotations
 
@@ -23,7 +25,10 @@ import torch
 __all__ = ["gdn_prefill", "gdn_decode_step", "gdn_decode_step_bf16_state", "gdn_decode_step_slots",
            "gdn_short_conv_norm", "gdn_prefill_conv", "gdn_prefill_conv_workspace_bytes",
            "gdn_prefill_host", "gdn_prefill_host_scratch_bytes", "gdn_prefill_slots",
-           "gdn_prefill_workspace_bytes", "library",
+           "gdn_prefill_workspace_bytes", "gdn_linear_prefill", "gdn_linear_prefill_slots",
+           "gdn_linear_prefill_backward", "gdn_linear_decode_step", "gdn_linear_decode_step_slots",
+           "gdn_linear_prefill_workspace_bytes", "gdn_linear_prefill_backward_workspace_bytes",
+           "gdn_qk_norm_rope", "gdn_qk_norm_rope_backward", "library",
            "GdnError", "LIB_PATH", "STATUS", "KERNELS"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdn.so")
@@ -99,6 +104,32 @@ def library():
             lib.gdn_prefill_ex_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i32, i32,
                                                            ctypes.c_int]
             lib.gdn_prefill_ex_workspace_bytes.restype = sz
+            f32, cint = ctypes.c_float, ctypes.c_int
+            sizes = [i32, i64, i32, i32, i32, i32]  # N, T, Hqk, Hv, Dk, Dv
+            lib.gdn_linear_prefill.argtypes = [vp, vp, vp, cint, vp, f32, vp, vp, *sizes, vp, vp, vp,
+                                               sz, vp, vp]
+            lib.gdn_linear_prefill_slots.argtypes = [vp, vp, vp, cint, vp, f32, vp, i32, vp, vp, vp,
+                                                     *sizes, vp, vp, sz, vp, vp]
+            lib.gdn_linear_prefill_backward.argtypes = [vp, vp, vp, vp, cint, vp, f32, vp, vp, vp,
+                                                        *sizes, vp, vp, vp, vp, vp, sz, vp, vp]
+            lib.gdn_linear_decode_step.argtypes = [vp, vp, vp, cint, vp, f32, vp, i32, i32, i32, i32,
+                                                   i32, vp, vp, vp]
+            lib.gdn_linear_decode_step_slots.argtypes = [vp, vp, vp, cint, vp, f32, vp, i32, vp, vp,
+                                                         i32, i32, i32, i32, i32, vp, vp, vp]
+            rope = [cint, i64, i64, vp, vp, f32, vp, i32, vp, vp, i32, i32, i64, i32, i32, i32]
+            lib.gdn_qk_norm_rope.argtypes = [vp, vp, *rope, vp, vp, vp]
+            lib.gdn_qk_norm_rope_backward.argtypes = [vp, vp, vp, vp, *rope, vp, vp, i64, i64, vp, vp,
+                                                      vp, sz, vp]
+            for fn in (lib.gdn_linear_prefill, lib.gdn_linear_prefill_slots,
+                       lib.gdn_linear_prefill_backward, lib.gdn_linear_decode_step,
+                       lib.gdn_linear_decode_step_slots, lib.gdn_qk_norm_rope,
+                       lib.gdn_qk_norm_rope_backward):
+                fn.restype = cint
+            for fn in (lib.gdn_linear_prefill_workspace_bytes,
+                       lib.gdn_linear_prefill_backward_workspace_bytes):
+                fn.argtypes, fn.restype = [*sizes, cint], sz
+            lib.gdn_qk_norm_rope_backward_workspace_bytes.argtypes = [i32]
+            lib.gdn_qk_norm_rope_backward_workspace_bytes.restype = sz
             lib.gdn_status_string.argtypes = [ctypes.c_int]
             lib.gdn_status_string.restype = ctypes.c_char_p
             lib.gdn_version.argtypes = []
@@ -506,3 +537,10 @@ def gdn_prefill_conv(xq, xk, xv, wq, wk, wv, g, beta, initial_state=None, cu_seq
     if conv_state_out is not None:
         return o, final_state, conv_state_out
     return o, final_state
+
+
+from .linear import (gdn_linear_decode_step, gdn_linear_decode_step_slots,  # noqa: E402
+                     gdn_linear_prefill, gdn_linear_prefill_backward,
+                     gdn_linear_prefill_backward_workspace_bytes, gdn_linear_prefill_slots,
+                     gdn_linear_prefill_workspace_bytes)
+from .rope import gdn_qk_norm_rope, gdn_qk_norm_rope_backward  # noqa: E402

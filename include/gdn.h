@@ -530,6 +530,185 @@ GDN_API size_t gdn_prefill_host_scratch_bytes(int64_t T, int32_t Hqk, int32_t Hv
                                               int64_t segment_tokens);
 
 /*
+ * Linear attention with a decay per head.  Section 三 of the page above starts
+ * from linear attention, the state S = sum of v k^T read out by the query; the
+ * calls below decay that state by a constant of the head at every token:
+ *
+ *     S_t = lam S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t,   lam = exp(log_decay[h])
+ *
+ * Layouts, head sharing, packing, ownership and errors are those of the gated
+ * delta rule's calls above.  log_decay is fp32 [Hv], finite and <= 0 (0: no
+ * decay); it is a constant of the layer, no call gives a gradient for it.
+ * scale multiplies the outputs only, never the state.  Sums and states are
+ * fp32; bf16 outputs are rounded once.  Dk and Dv in {16, 32, 64, 128}, either
+ * dtype; T < 2^31.
+ */
+
+/*
+ * gdn_linear_prefill -- the outputs and final states of a packed batch.
+ *   q, k, v, io_dtype, cu_seqlens, N, T, Hqk, Hv, Dk, Dv, dev_error_flag, stream
+ *                       as gdn_prefill.
+ *   initial_state       fp32 [N][Hv][Dv][Dk], or NULL for zeros.
+ *   o                   output [T][Hv][Dv] in io_dtype.
+ *   final_state         fp32 [N][Hv][Dv][Dk], or NULL to skip.  May equal
+ *                       initial_state (in place).  An empty sequence's final
+ *                       state is its initial state.
+ *   workspace, workspace_bytes
+ *                       device scratch of at least
+ *                       gdn_linear_prefill_workspace_bytes(), caller-owned,
+ *                       16-byte aligned; contents need not be preserved, and
+ *                       one workspace must not serve two calls at a time (two
+ *                       captured graphs that may run together included).
+ */
+GDN_API gdn_status gdn_linear_prefill(const void *q, const void *k, const void *v,
+                                      gdn_dtype io_dtype, const float *log_decay, float scale,
+                                      const float *initial_state, const int32_t *cu_seqlens,
+                                      int32_t N, int64_t T, int32_t Hqk, int32_t Hv, int32_t Dk,
+                                      int32_t Dv, void *o, float *final_state, void *workspace,
+                                      size_t workspace_bytes, int32_t *dev_error_flag,
+                                      void *stream);
+
+/* Scratch bytes gdn_linear_prefill and gdn_linear_prefill_slots need for these
+ * sizes (0 for none, or invalid ones). */
+GDN_API size_t gdn_linear_prefill_workspace_bytes(int32_t N, int64_t T, int32_t Hqk, int32_t Hv,
+                                                  int32_t Dk, int32_t Dv, gdn_dtype io_dtype);
+
+/*
+ * gdn_linear_prefill_slots -- gdn_linear_prefill over a pool of state slots, as
+ * gdn_prefill_slots is of gdn_prefill: sequence n starts from
+ * state_pool[slot_idx[n]] (from zeros when reset[n] is nonzero) and its final
+ * state goes back there.  state_pool is fp32 [num_slots][Hv][Dv][Dk]; slot_idx,
+ * reset (or NULL) are device int32 [N], slot_idx with distinct values.  An
+ * index out of range is reported as GDN_ERR_BAD_SLOT through dev_error_flag;
+ * that sequence runs from zeros and its state is not stored.
+ */
+GDN_API gdn_status gdn_linear_prefill_slots(const void *q, const void *k, const void *v,
+                                            gdn_dtype io_dtype, const float *log_decay, float scale,
+                                            float *state_pool, int32_t num_slots,
+                                            const int32_t *slot_idx, const int32_t *reset,
+                                            const int32_t *cu_seqlens, int32_t N, int64_t T,
+                                            int32_t Hqk, int32_t Hv, int32_t Dk, int32_t Dv,
+                                            void *o, void *workspace, size_t workspace_bytes,
+                                            int32_t *dev_error_flag, void *stream);
+
+/*
+ * gdn_linear_prefill_backward -- the gradients of gdn_linear_prefill, given
+ * those of its outputs.
+ *   dO                  [T][Hv][Dv] io_dtype, the gradient of o.
+ *   dfinal_state        fp32 [N][Hv][Dv][Dk], the gradient of final_state, or
+ *                       NULL for zeros.
+ *   q, k, v, log_decay, scale, initial_state, cu_seqlens and the sizes
+ *                       as in the forward call.
+ *   dq, dk, dv          outputs in io_dtype, shaped as q, k, v.  dq and dk sum
+ *                       over the v-heads that share the q/k head, in fp32 and
+ *                       in a fixed order.
+ *   dinitial_state      fp32 [N][Hv][Dv][Dk], the gradient of initial_state,
+ *                       or NULL to skip.  May equal dfinal_state (in place).
+ *   workspace, workspace_bytes
+ *                       as gdn_linear_prefill, sized by
+ *                       gdn_linear_prefill_backward_workspace_bytes().
+ */
+GDN_API gdn_status gdn_linear_prefill_backward(const void *dO, const void *q, const void *k,
+                                               const void *v, gdn_dtype io_dtype,
+                                               const float *log_decay, float scale,
+                                               const float *initial_state,
+                                               const float *dfinal_state,
+                                               const int32_t *cu_seqlens, int32_t N, int64_t T,
+                                               int32_t Hqk, int32_t Hv, int32_t Dk, int32_t Dv,
+                                               void *dq, void *dk, void *dv, float *dinitial_state,
+                                               void *workspace, size_t workspace_bytes,
+                                               int32_t *dev_error_flag, void *stream);
+
+/* Scratch bytes gdn_linear_prefill_backward needs for these sizes. */
+GDN_API size_t gdn_linear_prefill_backward_workspace_bytes(int32_t N, int64_t T, int32_t Hqk,
+                                                           int32_t Hv, int32_t Dk, int32_t Dv,
+                                                           gdn_dtype io_dtype);
+
+/*
+ * gdn_linear_decode_step -- one token of N sequences, in place on the states:
+ * S <- lam S + v k^T, o = scale S q.  Arguments as gdn_decode_step, with
+ * log_decay [Hv] and scale in place of g and beta.  Supported: Dk in
+ * {16, 32, 64, 128}, any Dv >= 1, either dtype.
+ */
+GDN_API gdn_status gdn_linear_decode_step(const void *q, const void *k, const void *v,
+                                          gdn_dtype io_dtype, const float *log_decay, float scale,
+                                          float *state, int32_t N, int32_t Hqk, int32_t Hv,
+                                          int32_t Dk, int32_t Dv, void *o, int32_t *dev_error_flag,
+                                          void *stream);
+
+/*
+ * gdn_linear_decode_step_slots -- gdn_linear_decode_step over a pool of state
+ * slots; state_pool, num_slots, slot_idx, reset and their errors as
+ * gdn_decode_step_slots.
+ */
+GDN_API gdn_status gdn_linear_decode_step_slots(const void *q, const void *k, const void *v,
+                                                gdn_dtype io_dtype, const float *log_decay,
+                                                float scale, float *state_pool, int32_t num_slots,
+                                                const int32_t *slot_idx, const int32_t *reset,
+                                                int32_t N, int32_t Hqk, int32_t Hv, int32_t Dk,
+                                                int32_t Dv, void *o, int32_t *dev_error_flag,
+                                                void *stream);
+
+/*
+ * gdn_qk_norm_rope -- the queries and keys of a linear attention (or attention)
+ * layer: RMS norm of every (token, head) row, then the rotation of its first
+ * `rot` dimensions by the token's positions, in one pass.  For a row x,
+ *     y = x (mean(x^2) + eps)^(-1/2) w,   z = Rot(y);
+ * Rot turns the pair of frequency i by positions[axis(i)][t] inv_freq[i].
+ *
+ *   xq, xk              [T][Hq][D], [T][Hk][D] io_dtype, contiguous within a
+ *                       token; xq_stride, xk_stride are the elements from one
+ *                       token to the next (Hq * D, Hk * D when packed; larger
+ *                       when they are parts of one projection), a multiple of
+ *                       16 bytes.  Hk may be 0 (xk, wk and k are then unused).
+ *   wq, wk              fp32 [D] weights, or NULL for ones.
+ *   eps                 > 0.
+ *   positions           int32 [axes][T], any values; axes <= 4.
+ *   sections            HOST int32 [axes], frequencies per axis in order,
+ *                       summing to rot / 2 (several axes: time, height and
+ *                       width of images and video); NULL when axes is 1.
+ *   inv_freq            fp32 [rot / 2].  Angles are exact to fp32 rounding at
+ *                       any position.
+ *   rot                 rotated dimensions, a multiple of 16, 0 .. D (0: norm
+ *                       alone; positions and inv_freq are then unused).
+ *   interleaved         0: the pair of frequency i is (y[i], y[i + rot/2]);
+ *                       1: (y[2i], y[2i + 1]).
+ *   q, k                outputs [T][Hq][D], [T][Hk][D] io_dtype, contiguous;
+ *                       computed in fp32, rounded once.
+ * Supported: D in {16, 32, 64, 128, 256}, either dtype.
+ */
+GDN_API gdn_status gdn_qk_norm_rope(const void *xq, const void *xk, gdn_dtype io_dtype,
+                                    int64_t xq_stride, int64_t xk_stride, const float *wq,
+                                    const float *wk, float eps, const int32_t *positions,
+                                    int32_t axes, const int32_t *sections, const float *inv_freq,
+                                    int32_t rot, int32_t interleaved, int64_t T, int32_t Hq,
+                                    int32_t Hk, int32_t D, void *q, void *k, void *stream);
+
+/*
+ * gdn_qk_norm_rope_backward -- its gradients.
+ *   dq, dk              gradients of q and k, [T][Hq][D], [T][Hk][D] io_dtype,
+ *                       contiguous.
+ *   dxq, dxk            outputs: gradients of xq and xk, io_dtype, with token
+ *                       strides dxq_stride, dxk_stride.
+ *   dwq, dwk            outputs fp32 [D]: gradients of the weights (of implied
+ *                       ones too), each or both NULL to skip; summed in fp32 in
+ *                       a fixed order.
+ *   workspace           gdn_qk_norm_rope_backward_workspace_bytes(D) of device
+ *                       scratch; may be NULL when dwq and dwk are.
+ *   everything else     as gdn_qk_norm_rope.
+ */
+GDN_API gdn_status gdn_qk_norm_rope_backward(
+    const void *dq, const void *dk, const void *xq, const void *xk, gdn_dtype io_dtype,
+    int64_t xq_stride, int64_t xk_stride, const float *wq, const float *wk, float eps,
+    const int32_t *positions, int32_t axes, const int32_t *sections, const float *inv_freq,
+    int32_t rot, int32_t interleaved, int64_t T, int32_t Hq, int32_t Hk, int32_t D, void *dxq,
+    void *dxk, int64_t dxq_stride, int64_t dxk_stride, float *dwq, float *dwk, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+/* Scratch bytes gdn_qk_norm_rope_backward needs for weight gradients. */
+GDN_API size_t gdn_qk_norm_rope_backward_workspace_bytes(int32_t D);
+
+/*
  * gdn_debug_prefill_pool_stall -- FOR TESTING THE TIMEOUT PATH ONLY.
  * gdn_prefill_ex with kernel GDN_PREFILL_POOL, except that the producer CTAs
  * never prepare the chunks of (sequence, head) unit `skip_unit` (n * Hv + h),

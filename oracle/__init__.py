@@ -350,3 +350,95 @@ def compose_state_maps(first, second):
     sequence's chunk maps can be combined by a parallel scan."""
     (A1, B1), (A2, B2) = first, second
     return A1 @ A2, B1 @ A2 + B2
+
+
+def _cu(cu_seqlens, T):
+    if cu_seqlens is None:
+        return np.array([0, T], dtype=np.int64)
+    return np.asarray(cu_seqlens.detach().cpu().numpy() if hasattr(cu_seqlens, "detach")
+                      else cu_seqlens, dtype=np.int64)
+
+
+def linear_recurrent(q, k, v, log_decay, s0=None, cu_seqlens=None, *, scale=1.0):
+    """Linear attention with a decay per head, token by token in float64:
+    S <- exp(log_decay[h]) S + v k^T, o = scale S q.  q, k [T,Hqk,Dk], v [T,Hv,Dv],
+    log_decay [Hv], s0 [N,Hv,Dv,Dk] or None.  Returns (o, final states)."""
+    q, k, v = _f64(q), _f64(k), _f64(v)
+    T, Hv, Dv = v.shape
+    G, Dk = Hv // q.shape[1], q.shape[2]
+    cu = _cu(cu_seqlens, T)
+    N = len(cu) - 1
+    lam = np.exp(_f64(log_decay))[:, None, None]
+    S = np.zeros((N, Hv, Dv, Dk)) if s0 is None else _f64(s0).copy()
+    o = np.zeros((T, Hv, Dv))
+    for n in range(N):
+        for t in range(cu[n], cu[n + 1]):
+            kt, qt = np.repeat(k[t], G, axis=0), np.repeat(q[t], G, axis=0)
+            S[n] = lam * S[n] + v[t][:, :, None] * kt[:, None, :]
+            o[t] = scale * np.einsum("hij,hj->hi", S[n], qt)
+    return o, S
+
+
+def linear_backward(do, q, k, v, log_decay, s0=None, cu_seqlens=None, *, dsT=None, scale=1.0):
+    """Gradients of linear_recurrent by its adjoint recurrence, float64:
+    G_t = dL/dS_t = scale do_t q_t^T + lam G_{t+1} (dsT joins at the last token);
+    dq_t = scale S_t^T do_t, dk_t = G_t^T v_t, dv_t = G_t k_t, ds0 = lam G_0 (dsT
+    itself for an empty sequence).  Returns (dq, dk, dv, ds0)."""
+    do, q, k, v = _f64(do), _f64(q), _f64(k), _f64(v)
+    T, Hv, Dv = v.shape
+    Hqk, Dk = q.shape[1:]
+    gr = Hv // Hqk
+    cu = _cu(cu_seqlens, T)
+    N = len(cu) - 1
+    lam = np.exp(_f64(log_decay))[:, None, None]
+    S = np.zeros((N, Hv, Dv, Dk)) if s0 is None else _f64(s0).copy()
+    G = np.zeros((N, Hv, Dv, Dk)) if dsT is None else _f64(dsT).copy()
+    dq, dk, dv = np.zeros((T, Hv, Dk)), np.zeros((T, Hv, Dk)), np.zeros((T, Hv, Dv))
+    for n in range(N):
+        for t in range(cu[n], cu[n + 1]):
+            S[n] = lam * S[n] + v[t][:, :, None] * np.repeat(k[t], gr, axis=0)[:, None, :]
+            dq[t] = scale * np.einsum("hij,hi->hj", S[n], do[t])
+        for t in range(cu[n + 1] - 1, cu[n] - 1, -1):
+            G[n] += scale * do[t][:, :, None] * np.repeat(q[t], gr, axis=0)[:, None, :]
+            dk[t] = np.einsum("hij,hi->hj", G[n], v[t])
+            dv[t] = np.einsum("hij,hj->hi", G[n], np.repeat(k[t], gr, axis=0))
+            G[n] *= lam
+    return dq.reshape(T, Hqk, gr, Dk).sum(2), dk.reshape(T, Hqk, gr, Dk).sum(2), dv, G
+
+
+def qk_norm_rope(x, w, eps, positions, inv_freq, *, sections=None, interleaved=False, inverse=False,
+                 norm=True):
+    """RMS norm of every row of x [T,H,D] times w [D] (or None), then the rotation
+    of the first 2 len(inv_freq) dimensions, float64.  positions [T] or [axes,T]
+    with sections.  ``inverse`` turns back, ``norm=False`` only turns."""
+    y = _f64(x)
+    if norm:
+        y = y / np.sqrt(np.mean(y * y, axis=-1, keepdims=True) + eps)
+        if w is not None:
+            y = y * _f64(w)
+    if inv_freq is None:
+        return y
+    f, pos = _f64(inv_freq), np.atleast_2d(_f64(positions))
+    h = f.shape[0]
+    axis = np.repeat(np.arange(pos.shape[0]), [h] if sections is None else sections)
+    ang = pos[axis].T * f  # [T, h]
+    u = np.exp((-1j if inverse else 1j) * ang)[:, None]
+    y = y.copy()
+    if interleaved:
+        z = (y[..., 0:2 * h:2] + 1j * y[..., 1:2 * h:2]) * u
+        y[..., 0:2 * h:2], y[..., 1:2 * h:2] = z.real, z.imag
+    else:
+        z = (y[..., :h] + 1j * y[..., h:2 * h]) * u
+        y[..., :h], y[..., h:2 * h] = z.real, z.imag
+    return y
+
+
+def qk_norm_rope_backward(dz, x, w, eps, positions, inv_freq, *, sections=None, interleaved=False):
+    """Gradients (dx, dw) of qk_norm_rope, float64."""
+    dy = qk_norm_rope(dz, None, eps, positions, inv_freq, sections=sections, interleaved=interleaved,
+                      inverse=True, norm=False)
+    x = _f64(x)
+    r = 1.0 / np.sqrt(np.mean(x * x, axis=-1, keepdims=True) + eps)
+    n = x * r
+    dn = dy if w is None else dy * _f64(w)
+    return r * (dn - n * np.mean(dn * n, axis=-1, keepdims=True)), np.sum(dy * n, axis=(0, 1))
