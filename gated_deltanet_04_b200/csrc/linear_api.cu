@@ -1,6 +1,6 @@
 // C entry points of linear attention with a decay per head: argument
 // validation and dispatch (include/gdn.h has the contracts).
-#include "linear.cuh"
+#include "linear_tc.cuh"
 #include "trace.cuh"
 
 namespace {
@@ -59,8 +59,13 @@ size_t seg_bytes(const Call &c, int64_t seg_len) {
     return seg_len ? al256((size_t)gdn::linear::slots_of(c.T, c.N, seg_len) * c.Hv * c.Dk * c.Dv * 4) : 0;
 }
 
+// The tensor-core kernels serve 128-wide bf16 heads.
+bool tensor_cores(const Call &c) { return c.dt == GDN_DTYPE_BF16 && c.Dk == 128 && c.Dv == 128 && c.T > 0; }
+
 size_t prefill_bytes(const Call &c) {
     if (check(c) != GDN_OK || check_size(c) != GDN_OK || c.T == 0) return 0;
+    if (tensor_cores(c))
+        return gdn::linear::state_dump_bytes(c.N, c.T, c.Hv) + gdn::linear::state_seg_bytes(c.N, c.T, c.Hv);
     return seg_bytes(c, gdn::linear::recurrent_seg_len(c.N, c.T, c.Hv, c.Dk, c.Dv));
 }
 
@@ -92,6 +97,20 @@ gdn_status prefill(const void *q, const void *k, const void *v, const float *log
     const size_t need = prefill_bytes(c);
     if (need > 0 && (ws == nullptr || ws_bytes < need)) return GDN_ERR_INVALID_ARGUMENT;
     if (c.N == 0 || (c.T == 0 && sT == nullptr)) return GDN_OK;  // nothing observable to do
+    if (tensor_cores(c)) {
+        gdn::linear::StatePass st{};
+        st.x = v; st.y = k; st.H = c.Hv; st.Hy = c.Hqk; st.log_decay = log_decay; st.x_scale = 1.f;
+        st.m0 = s0; st.mT = sT; st.map = map; st.cu = c.cu; st.N = c.N; st.T = c.T; st.err = err;
+        st.dump = static_cast<uint8_t *>(ws);
+        st.seg_chunks = gdn::linear::state_seg_chunks(c.N, c.T, c.Hv);
+        st.seg = st.seg_chunks
+                     ? reinterpret_cast<float *>(st.dump + gdn::linear::state_dump_bytes(c.N, c.T, c.Hv))
+                     : nullptr;
+        const cudaError_t e = gdn::linear::launch_states(st, s);
+        if (e != cudaSuccess) return from_cuda(e);
+        return from_cuda(gdn::linear::launch_out({q, k, v, o, st.dump, log_decay, scale, c.cu, c.N, c.T, c.Hqk,
+                                                  c.Hv, err}, s));
+    }
     Pass p{};
     p.a = q; p.b = k; p.c = v; p.out = o;
     p.Ha = c.Hqk; p.Hb = c.Hqk; p.Hc = c.Hv; p.Hout = c.Hv; p.H = c.Hv; p.Da = c.Dk; p.Dc = c.Dv;

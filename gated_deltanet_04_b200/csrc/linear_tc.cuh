@@ -1,0 +1,137 @@
+// What the tensor-core kernels of linear attention share (Dk = Dv = 128, bf16,
+// chunks of 128 tokens): tile constants, descriptors, bounded waits.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "linear.cuh"
+#include "sm100.cuh"
+
+namespace gdn {
+
+// [T][H][128] bf16 tensor map with 64 x 1 x `rows` boxes and the 128-byte
+// swizzle (rows past T read as zeros).
+bool make_tile_map_bf16_128(CUtensorMap *m, const void *base, int64_t T, int32_t H, int32_t rows);
+
+namespace linear {
+
+using namespace sm100;
+
+constexpr int kC = 128;                  // chunk length
+constexpr int kD = 128;                  // Dk = Dv
+constexpr uint32_t kSub = 16384;         // 128 rows x 64 columns of a tile, 128-byte swizzle
+constexpr uint32_t kTile = 2 * kSub;     // 128 x 128 bf16
+constexpr long long kWaitLimit = 1ll << 31;  // SM clocks (about a second)
+constexpr float kLog2e = 1.4426950408889634f;
+
+// bf16 operands, M = N = 128; letters: A then B, K-major or MN-major.
+constexpr uint32_t IDESC_KK = make_idesc_f16(128, 128, 0, 0, 1);
+constexpr uint32_t IDESC_KM = make_idesc_f16(128, 128, 0, 1, 1);
+constexpr uint32_t IDESC_MM = make_idesc_f16(128, 128, 1, 1, 1);
+
+// Descriptor of step ks (16 of the 128 summed elements) of a tile stored
+// [128 rows][128 columns]: rows are the operand's M (or N) index and columns the
+// summed one, or the other way round.
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int ks) {
+    return make_sdesc(tile + (ks >> 2) * kSub + (ks & 3) * 32, 16, 1024);
+}
+__device__ __forceinline__ uint64_t desc_m(uint32_t tile, int ks) {
+    return make_sdesc(tile + ks * 2048, kSub, 1024);
+}
+
+// D (+)= A B over 128 summed elements, operands in shared memory.
+__device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t b, bool acc) {
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) mma_f16_ss(d, desc_k(a, ks), desc_k(b, ks), IDESC_KK, acc || ks);
+}
+__device__ __forceinline__ void mma_km(uint32_t d, uint32_t a, uint32_t b, bool acc) {
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) mma_f16_ss(d, desc_k(a, ks), desc_m(b, ks), IDESC_KM, acc || ks);
+}
+__device__ __forceinline__ void mma_mm(uint32_t d, uint32_t a, uint32_t b, bool acc) {
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) mma_f16_ss(d, desc_m(a, ks), desc_m(b, ks), IDESC_MM, acc || ks);
+}
+// A from tensor memory (K-major, 64 columns of packed pairs), B MN-major.
+__device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a_tmem, uint32_t b, bool acc) {
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) mma_f16_ts(d, a_tmem + 8 * ks, desc_m(b, ks), IDESC_KM, acc || ks);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&t);
+}
+
+// Both 64-column halves of the 128-token tile of head h at token t0.
+__device__ __forceinline__ void load_tile(void *dst, const CUtensorMap *map, uint64_t *bar, int h, int64_t t0) {
+    tma_load_3d(dst, map, bar, 0, h, (int32_t)t0);
+    tma_load_3d(static_cast<uint8_t *>(dst) + kSub, map, bar, 64, h, (int32_t)t0);
+}
+
+// Waits of the warp-specialised kernels: give up when another role has
+// (`abort`), or after kWaitLimit clocks, raising `abort` and the error flag.
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, volatile int32_t *abort, int32_t *err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort) return false;
+        if (clock64() - t0 > kWaitLimit) {
+            *abort = 1;
+            raise_error(err, GDN_ERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// The states entering every chunk, found by one pass over a value-like array x
+// [T][H][128] and a key-like one y [T][Hy][128]:
+//   ascending   M' = lam^L M + sum_j lam^{L-1-j} x_j y_j^T       (S: x = v, y = k)
+//   descending  M' = lam^L M + x_scale sum_j lam^{j+1} x_j y_j^T  (G: x = do, y = q)
+// over chunks of L <= 128 tokens.  Every chunk's entering M goes, rounded to
+// bf16, to `dump` as the shared-memory image of a 128 x 128 tile (32 KB per
+// (chunk slot, head)); the last M in fp32 to mT.
+struct StatePass {
+    const void *x, *y;
+    int32_t H, Hy;
+    const float *log_decay;
+    float x_scale;
+    bool reverse;
+    const float *m0;
+    float *mT;
+    StateMap map;
+    const int32_t *cu;
+    int32_t N;
+    int64_t T;
+    int32_t *err;
+    float *seg;          // [seg slots][H][128][128] or null
+    int64_t seg_chunks;  // chunks per segment
+    uint8_t *dump;
+};
+
+// Workspace of a StatePass besides its dump; the dump's bytes.
+int64_t state_seg_chunks(int32_t N, int64_t T, int32_t H);  // 0: one segment per sequence
+size_t state_seg_bytes(int32_t N, int64_t T, int32_t H);
+size_t state_dump_bytes(int32_t N, int64_t T, int32_t H);
+// Runs the pass (segment sums and scan first when p.seg is set).
+cudaError_t launch_states(const StatePass &p, cudaStream_t s);
+
+struct OutPass {
+    const void *q, *k, *v;
+    void *o;
+    const uint8_t *dump;  // S entering every chunk
+    const float *log_decay;
+    float scale;
+    const int32_t *cu;
+    int32_t N;
+    int64_t T;
+    int32_t Hqk, Hv;
+    int32_t *err;
+};
+cudaError_t launch_out(const OutPass &p, cudaStream_t s);
+
+int device_sms();
+
+}  // namespace linear
+}  // namespace gdn

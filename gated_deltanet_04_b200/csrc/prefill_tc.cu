@@ -792,19 +792,24 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-// [T][H][128] bf16 tensor map with 64 x 1 x 64 boxes and the 128-byte swizzle,
-// shared by the tensor-core prefill kernels.
-bool make_tile_map_bf16_128(CUtensorMap *m, const void *base, int64_t T, int32_t H) {
+// [T][H][128] bf16 tensor map with 64 x 1 x `rows` boxes and the 128-byte
+// swizzle, shared by the tensor-core kernels.
+bool make_tile_map_bf16_128(CUtensorMap *m, const void *base, int64_t T, int32_t H, int32_t rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)H, (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)H * kD * 2};
-    const cuuint32_t box[3] = {64, 1, 64};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same with 64-token boxes, the gated delta rule's chunks.
+bool make_tile_map_bf16_128(CUtensorMap *m, const void *base, int64_t T, int32_t H) {
+    return make_tile_map_bf16_128(m, base, T, H, 64);
 }
 
 // The same map with 8-token boxes (the tokens before a chunk, for the fused
