@@ -44,12 +44,6 @@ static_assert(kSmem <= 232448, "shared memory of an SM");
 // TMEM columns: Q K^T, two P (bf16 pairs), Oi, Ox.
 constexpr uint32_t TM_QK = 0, TM_P = 128, TM_OI = 256, TM_OX = 384;
 
-__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-
 // Loads the tiles of this CTA's items in the order the MMA warp uses them.
 __device__ void produce(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v, const OutPass &p,
                         int64_t items, uint8_t *sm, Misc *ms, int G) {
@@ -205,7 +199,7 @@ __device__ void epilogue(const OutPass &p, uint8_t *sm, Misc *ms, uint32_t tmem,
 #pragma unroll
             for (int x = 0; x < 8; ++x)
                 w[x] = pack_bf16(fmaf(f, b[c + 2 * x], a[c + 2 * x]), fmaf(f, b[c + 2 * x + 1], a[c + 2 * x + 1]));
-            store32(dst + c, w);
+            store_b256(dst + c, w);
         }
         return true;
     };

@@ -52,10 +52,21 @@ __device__ __forceinline__ void mma_mm(uint32_t d, uint32_t a, uint32_t b, bool 
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) mma_f16_ss(d, desc_m(a, ks), desc_m(b, ks), IDESC_MM, acc || ks);
 }
-// A from tensor memory (K-major, 64 columns of packed pairs), B MN-major.
+// A from tensor memory (K-major, 64 columns of packed pairs), B MN-major or K-major.
 __device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a_tmem, uint32_t b, bool acc) {
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) mma_f16_ts(d, a_tmem + 8 * ks, desc_m(b, ks), IDESC_KM, acc || ks);
+}
+__device__ __forceinline__ void mma_tk(uint32_t d, uint32_t a_tmem, uint32_t b, bool acc) {
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) mma_f16_ts(d, a_tmem + 8 * ks, desc_k(b, ks), IDESC_KK, acc || ks);
+}
+
+// 32 bytes in one store: a whole memory sector per thread.
+__device__ __forceinline__ void store_b256(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -130,6 +141,20 @@ struct OutPass {
     int32_t *err;
 };
 cudaError_t launch_out(const OutPass &p, cudaStream_t s);
+
+struct BackwardPass {
+    const void *dO, *q, *k, *v;
+    void *dq, *dk, *dv;
+    const uint8_t *dump_s, *dump_g;  // S entering and G leaving every chunk
+    const float *log_decay;
+    float scale;
+    const int32_t *cu;
+    int32_t N;
+    int64_t T;
+    int32_t Hqk, Hv;
+    int32_t *err;
+};
+cudaError_t launch_backward(const BackwardPass &p, cudaStream_t s);
 
 int device_sms();
 
