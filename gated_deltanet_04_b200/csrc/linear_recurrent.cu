@@ -225,17 +225,31 @@ __global__ void gdn_linear_scan_kernel(Pass p) {
             cur = *reinterpret_cast<const float4 *>(src + x);
         }
     }
-    for (int64_t j = 0; j < count; ++j) {
-        const int64_t s = p.reverse ? count - 1 - j : j;
-        float4 *w = reinterpret_cast<float4 *>(p.seg + ((base + s) * p.H + h) * (int64_t)per + x);
-        const float4 own = j + 1 < count ? *w : make_float4(0.f, 0.f, 0.f, 0.f);
-        *w = cur;
-        const int64_t b = t0 + s * p.seg_len, e = b + p.seg_len < t1 ? b + p.seg_len : t1;
-        const float f = expf(g * (float)(e - b));
-        cur.x = fmaf(f, cur.x, own.x);
-        cur.y = fmaf(f, cur.y, own.y);
-        cur.z = fmaf(f, cur.z, own.z);
-        cur.w = fmaf(f, cur.w, own.w);
+    auto seg = [&](int64_t j) { return p.reverse ? count - 1 - j : j; };
+    auto at = [&](int64_t j) {
+        return reinterpret_cast<float4 *>(p.seg + ((base + seg(j)) * p.H + h) * (int64_t)per + x);
+    };
+    // sums a few segments ahead of the chain, so that their loads overlap
+    constexpr int kAhead = 4;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 own[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) own[i] = i + 1 < count ? *at(i) : zero;
+    for (int64_t j0 = 0; j0 < count; j0 += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int64_t j = j0 + i;
+            if (j >= count) break;
+            const float4 sum = own[i];
+            own[i] = j + kAhead + 1 < count ? *at(j + kAhead) : zero;
+            *at(j) = cur;
+            const int64_t b = t0 + seg(j) * p.seg_len, e = b + p.seg_len < t1 ? b + p.seg_len : t1;
+            const float f = expf(g * (float)(e - b));
+            cur.x = fmaf(f, cur.x, sum.x);
+            cur.y = fmaf(f, cur.y, sum.y);
+            cur.z = fmaf(f, cur.z, sum.z);
+            cur.w = fmaf(f, cur.w, sum.w);
+        }
     }
 }
 

@@ -1,39 +1,180 @@
 // Chunk states of linear attention on tensor cores (StatePass, linear_tc.cuh).
 //
 // One CTA walks the chunks of one (segment, head).  The state is held in
-// registers, fp32, 64 values of a row per thread; each chunk's sum of outer
+// registers, fp32, 32 values of a row per thread; each chunk's sum of outer
 // products is one fresh tensor-core accumulator added to it in fp32 (the tensor
 // core's own accumulation over thousands of chunks would truncate, and with a
 // slow decay the loss would add up).
 //
 // Precision: y enters as it is (bf16); x times its decay weight is split into
-// two bf16 parts, hi + lo, which keeps 16 bits of it (2^-17 relative on
-// average): two MMA passes instead of one, so that the fp32 states are good to
-// a few 1e-6.
+// bf16 parts, hi + mid + lo, which together keep fp32's 24 bits: three MMA
+// passes, wherever the sum goes into an fp32 state.  Where only bf16 images
+// come of it (a segment that does not end its sequence), hi + mid do.
 //
-// Per chunk: TMA brings x and y; the threads turn x in place into hi and write
-// lo beside it; the MMAs of chunk c run while the threads add chunk c - 1's
-// result to the state and store the image of the state that enters c.  Two
-// stages of (y, hi, lo) and the image take 224 KB of shared memory.
+// Roles, on stages of 64 tokens: a producer warp loads x and y by TMA into a
+// ring; 8 warps turn x in place into hi and write mid and lo beside it; an MMA
+// warp sums a chunk's stages into one of two accumulators; 16 warps add it to
+// the state and store the image of the state that enters the next chunk.
+// (One set of warps doing all of it in turn took twice as long: 3.3 us a chunk,
+// most of it waiting for loads issued one chunk ahead.)
 // Bound: HBM (64 KB in, 32 KB image out per chunk and head, y shared by the
-// heads of a group through L2) against 2 x 4.2 MFLOP on the tensor core.
+// heads of a group through L2) against two or three products of 4.2 MFLOP.
 #include "linear_tc.cuh"
 
 namespace gdn {
 namespace linear {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr uint32_t OFF_STAGE = 3 * kTile;  // y, x / hi, lo
-constexpr uint32_t OFF_IMAGE = 2 * OFF_STAGE;
+constexpr int kRows = 64;                    // tokens per stage
+constexpr uint32_t kHalf = kRows * 128;      // 64 rows x 64 columns
+constexpr uint32_t kPart = 2 * kHalf;        // 64 x 128 bf16
+constexpr int kRing = 4;
+constexpr int kStateWarps = 16, kConvWarps = 8;
+constexpr int kStateThreads = kStateWarps * 32, kConvThreads = kConvWarps * 32;
+constexpr int kThreads = kStateThreads + kConvThreads + 64;
+constexpr uint32_t OFF_PARTS = kRing * 2 * kPart;       // [2][mid, lo]
+constexpr uint32_t OFF_IMAGE = OFF_PARTS + 4 * kPart;
 constexpr uint32_t OFF_MISC = OFF_IMAGE + kTile;
 
 struct Misc {
-    uint64_t full[2], done[2];
+    uint64_t raw_full[kRing], raw_empty[kRing], part_full[2], part_empty[2], sum_full[2], sum_empty[2], drain;
     uint32_t tmem;
+    volatile int32_t abort;
 };
 constexpr uint32_t kSmem = OFF_MISC + sizeof(Misc) + 1024;
 static_assert(kSmem <= 232448, "shared memory of an SM");
+
+// The chunks of a segment in the pass's order.
+struct Walk {
+    int64_t t0, t1;
+    int nch;
+    bool reverse;
+    __device__ __forceinline__ int chunk(int it) const { return reverse ? nch - 1 - it : it; }
+    __device__ __forceinline__ int64_t start(int it) const { return t0 + (int64_t)chunk(it) * kC; }
+    __device__ __forceinline__ int length(int it) const {
+        const int64_t left = t1 - start(it);
+        return left < kC ? (int)left : kC;
+    }
+};
+
+__device__ void produce(const CUtensorMap &tm_x, const CUtensorMap &tm_y, const Walk &w, int h, int hy, uint8_t *sm,
+                        Misc *ms, int32_t *err) {
+    uint32_t r = 0;  // stages so far
+    for (int it = 0; it < w.nch; ++it) {
+        const int L = w.length(it);
+        for (int j0 = 0; j0 < L; j0 += kRows, ++r) {
+            const int b = r % kRing;
+            if (r >= kRing && !role_wait(&ms->raw_empty[b], (r / kRing - 1) & 1, &ms->abort, err)) {
+                // given up: let the loads in flight land before the CTA ends
+                for (uint32_t x = r - kRing; x < r; ++x)
+                    mbar_wait_bounded(&ms->raw_full[x % kRing], (x / kRing) & 1, kWaitLimit);
+                return;
+            }
+            uint8_t *y = sm + b * 2 * kPart, *x = y + kPart;
+            const int32_t t = (int32_t)(w.start(it) + j0);
+            mbar_arrive_expect_tx(&ms->raw_full[b], 2 * kPart);
+            tma_load_3d(x, &tm_x, &ms->raw_full[b], 0, h, t);
+            tma_load_3d(x + kHalf, &tm_x, &ms->raw_full[b], 64, h, t);
+            tma_load_3d(y, &tm_y, &ms->raw_full[b], 0, hy, t);
+            tma_load_3d(y + kHalf, &tm_y, &ms->raw_full[b], 64, hy, t);
+        }
+    }
+}
+
+// x w = hi + mid + lo: hi in place, the others into the parts buffer.
+__device__ void convert(const Walk &w, float l2, float x_scale, int parts, uint8_t *sm, Misc *ms, int tid,
+                        int32_t *err) {
+    const int r0 = tid >> 3, piece = (tid & 7) * 16;  // rows r0 and r0 + 32 of a stage
+    uint32_t r = 0;
+    // weight of row j of a chunk of L tokens (0 past its end)
+    auto weight = [&](int j, int L) {
+        if (j >= L) return 0.f;
+        return w.reverse ? x_scale * exp2f(l2 * (float)(j + 1)) : exp2f(l2 * (float)(L - 1 - j));
+    };
+    float wfull[4];  // of whole chunks
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wfull[i] = weight(r0 + 32 * i, kC);
+    for (int it = 0; it < w.nch; ++it) {
+        const int L = w.length(it);
+        for (int s = 0; s * kRows < L; ++s, ++r) {
+            const int b = r % kRing;
+            if (!role_wait(&ms->raw_full[b], (r / kRing) & 1, &ms->abort, err)) return;
+            if (r >= 2 && !role_wait(&ms->part_empty[r & 1], ((r >> 1) - 1) & 1, &ms->abort, err)) return;
+            uint8_t *y = sm + b * 2 * kPart, *x = y + kPart, *mid = sm + OFF_PARTS + (r & 1) * 2 * kPart;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = s * kRows + r0 + 32 * i;
+                const float f = L == kC ? (s ? wfull[2 + i] : wfull[i]) : weight(j, L);
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub) {
+                    const uint32_t at = sub * kHalf + (r0 + 32 * i) * 128 + piece;
+                    uint32_t a[4] = {0u, 0u, 0u, 0u}, m[4] = {0u, 0u, 0u, 0u}, l[4] = {0u, 0u, 0u, 0u};
+                    if (j < L) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(x + at);
+                        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float2 g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&in[q]));
+                            const float e0 = g.x * f, e1 = g.y * f;
+                            a[q] = pack_bf16(e0, e1);
+                            const float2 t = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&a[q]));
+                            const float d0 = e0 - t.x, d1 = e1 - t.y;
+                            m[q] = pack_bf16(d0, d1);
+                            if (parts == 3) {
+                                const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&m[q]));
+                                l[q] = pack_bf16(d0 - u.x, d1 - u.y);
+                            }
+                        }
+                    } else {  // rows of the next sequence: y too, or its NaN would reach this sum
+                        *reinterpret_cast<uint4 *>(y + at) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    *reinterpret_cast<uint4 *>(x + at) = make_uint4(a[0], a[1], a[2], a[3]);
+                    *reinterpret_cast<uint4 *>(mid + at) = make_uint4(m[0], m[1], m[2], m[3]);
+                    if (parts == 3) *reinterpret_cast<uint4 *>(mid + kPart + at) = make_uint4(l[0], l[1], l[2], l[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&ms->part_full[r & 1]);
+        }
+    }
+}
+
+// D (+)= x^T y over a stage's 64 tokens, both MN-major.
+__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t x, uint32_t y, bool acc) {
+#pragma unroll
+    for (int ks = 0; ks < kRows / 16; ++ks)
+        mma_f16_ss(d, make_sdesc(x + ks * 2048, kHalf, 1024), make_sdesc(y + ks * 2048, kHalf, 1024), IDESC_MM,
+                   acc || ks);
+}
+
+__device__ void multiply(const Walk &w, int parts, uint32_t sbase, uint32_t tmem, Misc *ms, int32_t *err) {
+    uint32_t r = 0;
+    bool ok = true;
+    for (int it = 0; ok && it < w.nch; ++it) {
+        const int L = w.length(it);
+        const uint32_t d = tmem + 128 * (it & 1);
+        if (it >= 2 && !(ok = role_wait(&ms->sum_empty[it & 1], ((it >> 1) - 1) & 1, &ms->abort, err))) break;
+        for (int j0 = 0; j0 < L; j0 += kRows, ++r) {
+            if (!(ok = role_wait(&ms->part_full[r & 1], (r >> 1) & 1, &ms->abort, err))) break;
+            tc_fence_after_sync();
+            const uint32_t y = sbase + (r % kRing) * 2 * kPart, mid = sbase + OFF_PARTS + (r & 1) * 2 * kPart;
+            mma_stage(d, y + kPart, y, j0 > 0);
+            mma_stage(d, mid, y, true);
+            if (parts == 3) mma_stage(d, mid + kPart, y, true);
+            mma_commit(&ms->raw_empty[r % kRing]);
+            mma_commit(&ms->part_empty[r & 1]);
+        }
+        if (ok) mma_commit(&ms->sum_full[it & 1]);
+    }
+    if (ok) return;
+    // given up: let the MMAs in flight finish before tensor memory is freed
+    mma_commit(&ms->drain);
+    mbar_wait_bounded(&ms->drain, 0, kWaitLimit);
+}
+
+__device__ __forceinline__ void state_barrier() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kStateThreads) : "memory");
+}
 
 // kDump: the pass proper (images, final state); otherwise the segments' sums.
 template <bool kDump>
@@ -43,9 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Misc *ms = reinterpret_cast<Misc *>(sm + OFF_MISC);
-    const uint32_t sbase = smem_u32(sm);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
-    const int row = quad * 32 + lane;  // row of M, its columns 64 half ..
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     const int h = blockIdx.x % p.H;
     const int64_t slot = blockIdx.x / p.H;
@@ -55,17 +194,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool last = p.reverse ? sp.s == 0 : sp.s == sp.count - 1;  // in the pass's order
     if (!kDump && last) return;  // nothing starts from its sum
     const int hy = h / (p.H / p.Hy);
-    const int nch = (int)((sp.t1 - sp.t0 + kC - 1) / kC);
+    const Walk w{sp.t0, sp.t1, (int)((sp.t1 - sp.t0 + kC - 1) / kC), p.reverse};
     const float l2 = p.log_decay[h] * kLog2e;
+    const int parts = kDump && !(last && p.mT) ? 2 : 3;
 
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&ms->full[s], 1);
-            mbar_init(&ms->done[s], 1);
+        for (int b = 0; b < kRing; ++b) {
+            mbar_init(&ms->raw_full[b], 1);
+            mbar_init(&ms->raw_empty[b], 1);
         }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ms->part_full[b], kConvThreads);
+            mbar_init(&ms->part_empty[b], 1);
+            mbar_init(&ms->sum_full[b], 1);
+            mbar_init(&ms->sum_empty[b], kStateThreads);
+        }
+        mbar_init(&ms->drain, 1);
+        ms->abort = 0;
         fence_mbarrier_init();
-        tma_prefetch_desc(&tm_x);
-        tma_prefetch_desc(&tm_y);
     }
     if (warp == 0) {
         tmem_alloc(&ms->tmem, 256);
@@ -75,155 +221,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = ms->tmem;
-    const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + 64 * half;
 
-    auto chunk_at = [&](int it) { return p.reverse ? nch - 1 - it : it; };
-    auto issue = [&](int it) {  // thread 0
-        uint8_t *st = sm + (it & 1) * OFF_STAGE;
-        const int64_t t = sp.t0 + (int64_t)chunk_at(it) * kC;
-        mbar_arrive_expect_tx(&ms->full[it & 1], 2 * kTile);
-        load_tile(st + kTile, &tm_x, &ms->full[it & 1], h, t);
-        load_tile(st, &tm_y, &ms->full[it & 1], hy, t);
-    };
-    int issued = 0;  // thread 0's count
-    if (tid == 0)
-        for (; issued < nch && issued < 2; ++issued) issue(issued);
-
-    float S[64];
-    const int64_t st = kDump ? state_index(p.map, sp.n) : 0;
-    if (kDump && st < 0 && tid == 0 && h == 0) raise_error(p.err, GDN_ERR_BAD_SLOT);
-    {
-        const float *src = nullptr;
-        if (kDump && p.seg) src = p.seg + ((slot * p.H + h) * kD + row) * (int64_t)kD + 64 * half;
-        else if (kDump && p.m0 && st >= 0 && !state_fresh(p.map, sp.n))
-            src = p.m0 + ((st * p.H + h) * kD + row) * (int64_t)kD + 64 * half;
-#pragma unroll
-        for (int x = 0; x < 64; x += 4) {
-            const float4 f = src ? *reinterpret_cast<const float4 *>(src + x) : make_float4(0.f, 0.f, 0.f, 0.f);
-            S[x] = f.x; S[x + 1] = f.y; S[x + 2] = f.z; S[x + 3] = f.w;
+    if (warp >= kStateWarps) {
+        if (warp < kStateWarps + kConvWarps)
+            convert(w, l2, p.x_scale, parts, sm, ms, tid - kStateThreads, p.err);
+        else if (warp == kStateWarps + kConvWarps) {
+            if (lane == 0) produce(tm_x, tm_y, w, h, hy, sm, ms, p.err);
+        } else if (lane == 0) {
+            multiply(w, parts, smem_u32(sm), tmem, ms, p.err);
         }
-    }
-    // weight of row j of a chunk of L tokens (0 past its end)
-    auto weight = [&](int j, int L) {
-        if (j >= L) return 0.f;
-        return p.reverse ? p.x_scale * exp2f(l2 * (float)(j + 1)) : exp2f(l2 * (float)(L - 1 - j));
-    };
-    float wfull[4];  // this thread converts rows tid / 8 + 32 i
-#pragma unroll
-    for (int i = 0; i < 4; ++i) wfull[i] = weight((tid >> 3) + 32 * i, kC);
-    const float dec_full = exp2f(l2 * (float)kC);
-
-    bool timed_out = false;
-    // S <- lam^L S + chunk it's sum, once its MMAs are done
-    auto finish = [&](int it) {
-        if (!mbar_wait_bounded(&ms->done[it & 1], (it >> 1) & 1, kWaitLimit)) timed_out = true;
-        tc_fence_after_sync();
-        const int64_t left = sp.t1 - (sp.t0 + (int64_t)chunk_at(it) * kC);
-        const float dec = left < kC ? exp2f(l2 * (float)left) : dec_full;
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-            float d[32];
-            tmem_ld32(trow + 128 * (it & 1) + c, d);
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 32; ++x) S[c + x] = fmaf(dec, S[c + x], d[x]);
-        }
-    };
-    int it = 0;
-#pragma unroll 1
-    for (; it < nch; ++it) {
-        uint8_t *stg = sm + (it & 1) * OFF_STAGE;
-        const int c = chunk_at(it);
-        const int64_t left = sp.t1 - (sp.t0 + (int64_t)c * kC);
-        const int L = left < kC ? (int)left : kC;
-        if (!mbar_wait_bounded(&ms->full[it & 1], (it >> 1) & 1, kWaitLimit)) timed_out = true;
-        // 16-byte pieces: rows tid / 8 + 32 i of both column halves
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = (tid >> 3) + 32 * i;
-            const float w = L == kC ? wfull[i] : weight(j, L);
-#pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
-                uint8_t *at = stg + kTile + sub * kSub + j * 128 + (tid & 7) * 16;
-                uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-                if (j < L) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(at);
-                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t oh[4], ol[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&in[q]));
-                        const float a = f.x * w, b = f.y * w;
-                        oh[q] = pack_bf16(a, b);
-                        const float2 r = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&oh[q]));
-                        ol[q] = pack_bf16(a - r.x, b - r.y);
-                    }
-                    hi = make_uint4(oh[0], oh[1], oh[2], oh[3]);
-                    lo = make_uint4(ol[0], ol[1], ol[2], ol[3]);
-                } else {
-                    // rows of the next sequence: y too, or its NaN would reach this sum
-                    *reinterpret_cast<uint4 *>(at - kTile) = hi;
-                }
-                *reinterpret_cast<uint4 *>(at) = hi;
-                *reinterpret_cast<uint4 *>(at + kTile) = lo;
-            }
-        }
-        fence_proxy_async_smem();
-        if (kDump && tid == 0) bulk_wait_read_all();  // the image buffer is free again
-        tc_fence_before_sync();
-        if (__syncthreads_or(timed_out ? 1 : 0)) break;
-        tc_fence_after_sync();
-        if (tid == 0) {
-            const uint32_t y = sbase + (it & 1) * OFF_STAGE, d = tmem + 128 * (it & 1);
-            mma_mm(d, y + kTile, y, false);
-            mma_mm(d, y + 2 * kTile, y, true);
-            mma_commit(&ms->done[it & 1]);
-        }
-        if (it > 0) {
-            finish(it - 1);
-            if (tid == 0 && issued < nch) {  // its stage is free
-                issue(issued);
-                ++issued;
-            }
-        }
-        if (kDump) {
-#pragma unroll
-            for (int x = 0; x < 64; x += 8) {
-                const uint4 v = make_uint4(pack_bf16(S[x], S[x + 1]), pack_bf16(S[x + 2], S[x + 3]),
-                                           pack_bf16(S[x + 4], S[x + 5]), pack_bf16(S[x + 6], S[x + 7]));
-                *reinterpret_cast<uint4 *>(sm + OFF_IMAGE + half * kSub + sw128(row, 2 * x)) = v;
-            }
-            fence_proxy_async_smem();
-            __syncthreads();
-            if (tid == 0) {
-                const int64_t cs = slot_base(p.cu, sp.n, kC) + (sp.t0 - (p.cu ? p.cu[sp.n] : 0)) / kC + c;
-                bulk_store(p.dump + (cs * p.H + h) * (int64_t)kTile, sm + OFF_IMAGE, kTile);
-                bulk_commit();
-            }
-        }
-    }
-    const bool ok = it == nch;
-    if (ok && nch > 0) finish(nch - 1);
-    if (!ok || timed_out) {
-        if (tid == 0) raise_error(p.err, GDN_ERR_TIMEOUT);
-        // a bounded chance for the MMAs and tile loads in flight to land
-        for (int s = 0; s < 2; ++s) {
-            const int k = it - 1 - ((it - 1 - s) & 1);  // the last chunk whose MMAs used barrier s
-            if (it > 0 && k >= 0) mbar_wait_bounded(&ms->done[s], (k >> 1) & 1, kWaitLimit);
-        }
-        if (tid == 0)
-            for (int k = it; k < issued; ++k) mbar_wait_bounded(&ms->full[k & 1], (k >> 1) & 1, kWaitLimit);
     } else {
+        const int quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane;  // columns 32 cg .. of row
+        const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + 32 * cg;
+        const int64_t st = kDump ? state_index(p.map, sp.n) : 0;
+        if (kDump && st < 0 && tid == 0 && h == 0) raise_error(p.err, GDN_ERR_BAD_SLOT);
+        const int64_t at = (int64_t)row * kD + 32 * cg;  // within a state
+        float S[32];
+        {
+            const float *src = nullptr;
+            if (kDump && p.seg) src = p.seg + (slot * p.H + h) * (int64_t)(kD * kD) + at;
+            else if (kDump && p.m0 && st >= 0 && !state_fresh(p.map, sp.n))
+                src = p.m0 + (st * p.H + h) * (int64_t)(kD * kD) + at;
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
+                const float4 f = src ? *reinterpret_cast<const float4 *>(src + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+                S[x] = f.x; S[x + 1] = f.y; S[x + 2] = f.z; S[x + 3] = f.w;
+            }
+        }
+        const float dec_full = exp2f(l2 * (float)kC);
+        uint8_t *image = sm + OFF_IMAGE + (cg >> 1) * kSub;
+        const int64_t chunk0 = kDump ? slot_base(p.cu, sp.n, kC) + sp.s * (seg_len / kC) : 0;
+        bool ok = true;
+        for (int it = 0; it < w.nch; ++it) {
+            if (kDump) {
+                if (tid == 0) bulk_wait_read_all();  // the image buffer is free again
+                state_barrier();
+#pragma unroll
+                for (int x = 0; x < 32; x += 8) {
+                    const uint4 v = make_uint4(pack_bf16(S[x], S[x + 1]), pack_bf16(S[x + 2], S[x + 3]),
+                                               pack_bf16(S[x + 4], S[x + 5]), pack_bf16(S[x + 6], S[x + 7]));
+                    *reinterpret_cast<uint4 *>(image + sw128(row, 64 * (cg & 1) + 2 * x)) = v;
+                }
+                fence_proxy_async_smem();
+                state_barrier();
+                if (tid == 0) {
+                    const int64_t cs = chunk0 + w.chunk(it);
+                    bulk_store(p.dump + (cs * p.H + h) * (int64_t)kTile, sm + OFF_IMAGE, kTile);
+                    bulk_commit();
+                }
+            }
+            // every warp goes on after a wait given up, so that the barriers above stay whole
+            if (ok) ok = role_wait(&ms->sum_full[it & 1], (it >> 1) & 1, &ms->abort, p.err);
+            tc_fence_after_sync();
+            const int L = w.length(it);
+            const float dec = L < kC ? exp2f(l2 * (float)L) : dec_full;
+            float d[32];
+            tmem_ld32(trow + 128 * (it & 1), d);
+            tmem_wait_ld();
+            tc_fence_before_sync();
+            mbar_arrive(&ms->sum_empty[it & 1]);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) S[x] = fmaf(dec, S[x], d[x]);
+        }
         float *dst = kDump ? (last && p.mT && st >= 0 ? p.mT + (st * p.H + h) * (int64_t)(kD * kD) : nullptr)
                            : p.seg + (slot * p.H + h) * (int64_t)(kD * kD);
-        if (dst) {
-            dst += (int64_t)row * kD + 64 * half;
+        if (ok && dst) {
 #pragma unroll
-            for (int x = 0; x < 64; x += 4)
-                *reinterpret_cast<float4 *>(dst + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
+            for (int x = 0; x < 32; x += 4)
+                *reinterpret_cast<float4 *>(dst + at + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
         }
+        if (kDump && tid == 0) bulk_wait_all();
     }
-    if (kDump && tid == 0) bulk_wait_all();
+    __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -275,7 +344,7 @@ size_t state_dump_bytes(int32_t N, int64_t T, int32_t H) { return (size_t)slots_
 cudaError_t launch_states(const StatePass &p, cudaStream_t s) {
     CUtensorMap mx, my;
     const int64_t Tm = p.T > 0 ? p.T : 1;
-    if (!make_tile_map_bf16_128(&mx, p.x, Tm, p.H, kC) || !make_tile_map_bf16_128(&my, p.y, Tm, p.Hy, kC))
+    if (!make_tile_map_bf16_128(&mx, p.x, Tm, p.H, kRows) || !make_tile_map_bf16_128(&my, p.y, Tm, p.Hy, kRows))
         return cudaErrorInvalidValue;
     if (p.seg) {
         cudaError_t e = launch<false>(mx, my, p, s);
