@@ -1,10 +1,10 @@
 // Chunk states of linear attention on tensor cores (StatePass, linear_tc.cuh).
 //
-// One CTA walks the chunks of one (segment, head).  The state is held in
-// registers, fp32, 32 values of a row per thread; each chunk's sum of outer
-// products is one fresh tensor-core accumulator added to it in fp32 (the tensor
-// core's own accumulation over thousands of chunks would truncate, and with a
-// slow decay the loss would add up).
+// One CTA walks the chunks of one (segment, head).  The fp32 state stays in
+// tensor memory; each chunk's sum of outer products is one fresh tensor-core
+// accumulator added to it by fp32 FMAs (the tensor core's own accumulation over
+// thousands of chunks would truncate, and with a slow decay the loss would add
+// up).
 //
 // Precision: y enters as it is (bf16); x times its decay weight is split into
 // bf16 parts, hi + mid + lo, which together keep fp32's 24 bits: three MMA
@@ -12,11 +12,11 @@
 // come of it (a segment that does not end its sequence), hi + mid do.
 //
 // Roles, on stages of 64 tokens: a producer warp loads x and y by TMA into a
-// ring; 8 warps turn x in place into hi and write mid and lo beside it; an MMA
-// warp sums a chunk's stages into one of two accumulators; 16 warps add it to
-// the state and store the image of the state that enters the next chunk.
-// (One set of warps doing all of it in turn took twice as long: 3.3 us a chunk,
-// most of it waiting for loads issued one chunk ahead.)
+// ring; two groups of 8 warps take stages in turn, turning x in place into hi
+// and writing mid and lo beside it (one group alone was bound by the latency of
+// its steps, 2.2 us a chunk with or without lo); an MMA warp sums a chunk's
+// stages into one of two accumulators; 8 warps add it to the state and store
+// the image of the state that enters the next chunk.
 // Bound: HBM (64 KB in, 32 KB image out per chunk and head, y shared by the
 // heads of a group through L2) against two or three products of 4.2 MFLOP.
 #include "linear_tc.cuh"
@@ -29,9 +29,10 @@ constexpr int kRows = 64;                    // tokens per stage
 constexpr uint32_t kHalf = kRows * 128;      // 64 rows x 64 columns
 constexpr uint32_t kPart = 2 * kHalf;        // 64 x 128 bf16
 constexpr int kRing = 4;
-constexpr int kStateWarps = 16, kConvWarps = 8;
+constexpr int kStateWarps = 8, kConvWarps = 8, kConvGroups = 2;
 constexpr int kStateThreads = kStateWarps * 32, kConvThreads = kConvWarps * 32;
-constexpr int kThreads = kStateThreads + kConvThreads + 64;
+constexpr int kThreads = kStateThreads + kConvGroups * kConvThreads + 64;
+constexpr uint32_t TM_S = 256;  // tensor memory: two sums, the state
 constexpr uint32_t OFF_PARTS = kRing * 2 * kPart;       // [2][mid, lo]
 constexpr uint32_t OFF_IMAGE = OFF_PARTS + 4 * kPart;
 constexpr uint32_t OFF_MISC = OFF_IMAGE + kTile;
@@ -81,11 +82,13 @@ __device__ void produce(const CUtensorMap &tm_x, const CUtensorMap &tm_y, const 
     }
 }
 
-// x w = hi + mid + lo: hi in place, the others into the parts buffer.
-__device__ void convert(const Walk &w, float l2, float x_scale, int parts, uint8_t *sm, Misc *ms, int tid,
+// x w = hi + mid + lo: hi in place, the others into the parts buffer of the
+// group, which takes every second stage.
+__device__ void convert(const Walk &w, float l2, float x_scale, int parts, uint8_t *sm, Misc *ms, int group, int tid,
                         int32_t *err) {
     const int r0 = tid >> 3, piece = (tid & 7) * 16;  // rows r0 and r0 + 32 of a stage
-    uint32_t r = 0;
+    const float2 minus = make_float2(-1.f, -1.f);
+    uint32_t r = 0;  // stages so far, of both groups
     // weight of row j of a chunk of L tokens (0 past its end)
     auto weight = [&](int j, int L) {
         if (j >= L) return 0.f;
@@ -97,6 +100,7 @@ __device__ void convert(const Walk &w, float l2, float x_scale, int parts, uint8
     for (int it = 0; it < w.nch; ++it) {
         const int L = w.length(it);
         for (int s = 0; s * kRows < L; ++s, ++r) {
+            if ((r & 1) != group) continue;
             const int b = r % kRing;
             if (!role_wait(&ms->raw_full[b], (r / kRing) & 1, &ms->abort, err)) return;
             if (r >= 2 && !role_wait(&ms->part_empty[r & 1], ((r >> 1) - 1) & 1, &ms->abort, err)) return;
@@ -114,16 +118,11 @@ __device__ void convert(const Walk &w, float l2, float x_scale, int parts, uint8
                         const uint32_t in[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const float2 g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&in[q]));
-                            const float e0 = g.x * f, e1 = g.y * f;
-                            a[q] = pack_bf16(e0, e1);
-                            const float2 t = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&a[q]));
-                            const float d0 = e0 - t.x, d1 = e1 - t.y;
-                            m[q] = pack_bf16(d0, d1);
-                            if (parts == 3) {
-                                const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&m[q]));
-                                l[q] = pack_bf16(d0 - u.x, d1 - u.y);
-                            }
+                            const float2 e = fmul2(unpack_bf16(in[q]), make_float2(f, f));
+                            a[q] = pack_bf16(e);
+                            const float2 d = ffma2(unpack_bf16(a[q]), minus, e);
+                            m[q] = pack_bf16(d);
+                            if (parts == 3) l[q] = pack_bf16(ffma2(unpack_bf16(m[q]), minus, d));
                         }
                     } else {  // rows of the next sequence: y too, or its NaN would reach this sum
                         *reinterpret_cast<uint4 *>(y + at) = make_uint4(0u, 0u, 0u, 0u);
@@ -214,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbarrier_init();
     }
     if (warp == 0) {
-        tmem_alloc(&ms->tmem, 256);
+        tmem_alloc(&ms->tmem, 512);
         tmem_relinquish();
     }
     tc_fence_before_sync();
@@ -223,72 +222,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = ms->tmem;
 
     if (warp >= kStateWarps) {
-        if (warp < kStateWarps + kConvWarps)
-            convert(w, l2, p.x_scale, parts, sm, ms, tid - kStateThreads, p.err);
-        else if (warp == kStateWarps + kConvWarps) {
+        const int cw = warp - kStateWarps;
+        if (cw < kConvGroups * kConvWarps)
+            convert(w, l2, p.x_scale, parts, sm, ms, cw / kConvWarps, (tid - kStateThreads) % kConvThreads, p.err);
+        else if (cw == kConvGroups * kConvWarps) {
             if (lane == 0) produce(tm_x, tm_y, w, h, hy, sm, ms, p.err);
         } else if (lane == 0) {
             multiply(w, parts, smem_u32(sm), tmem, ms, p.err);
         }
     } else {
-        const int quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane;  // columns 32 cg .. of row
-        const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + 32 * cg;
+        const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;  // columns 64 half .. of row
+        const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + 64 * half;
         const int64_t st = kDump ? state_index(p.map, sp.n) : 0;
         if (kDump && st < 0 && tid == 0 && h == 0) raise_error(p.err, GDN_ERR_BAD_SLOT);
-        const int64_t at = (int64_t)row * kD + 32 * cg;  // within a state
-        float S[32];
-        {
-            const float *src = nullptr;
-            if (kDump && p.seg) src = p.seg + (slot * p.H + h) * (int64_t)(kD * kD) + at;
-            else if (kDump && p.m0 && st >= 0 && !state_fresh(p.map, sp.n))
-                src = p.m0 + (st * p.H + h) * (int64_t)(kD * kD) + at;
+        const int64_t at = (int64_t)row * kD + 64 * half;  // within a state
+        uint8_t *image = sm + OFF_IMAGE + half * kSub;
+        // columns c .. c + 15 of this thread's half row of the image
+        auto draw = [&](int c, const float *v) {  // 16 of them
 #pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-                const float4 f = src ? *reinterpret_cast<const float4 *>(src + x) : make_float4(0.f, 0.f, 0.f, 0.f);
-                S[x] = f.x; S[x + 1] = f.y; S[x + 2] = f.z; S[x + 3] = f.w;
-            }
-        }
-        const float dec_full = exp2f(l2 * (float)kC);
-        uint8_t *image = sm + OFF_IMAGE + (cg >> 1) * kSub;
+            for (int x = 0; x < 16; x += 8)
+                *reinterpret_cast<uint4 *>(image + sw128(row, 2 * (c + x))) =
+                    make_uint4(pack_bf16(v[x], v[x + 1]), pack_bf16(v[x + 2], v[x + 3]),
+                               pack_bf16(v[x + 4], v[x + 5]), pack_bf16(v[x + 6], v[x + 7]));
+        };
         const int64_t chunk0 = kDump ? slot_base(p.cu, sp.n, kC) + sp.s * (seg_len / kC) : 0;
+        auto store_image = [&](int it) {  // the state entering chunk it; all state warps call
+            fence_proxy_async_smem();
+            state_barrier();
+            if (tid == 0) {
+                bulk_store(p.dump + ((chunk0 + w.chunk(it)) * p.H + h) * (int64_t)kTile, sm + OFF_IMAGE, kTile);
+                bulk_commit();
+            }
+        };
+        const float *src = nullptr;
+        if (kDump && p.seg) src = p.seg + (slot * p.H + h) * (int64_t)(kD * kD) + at;
+        else if (kDump && p.m0 && st >= 0 && !state_fresh(p.map, sp.n))
+            src = p.m0 + (st * p.H + h) * (int64_t)(kD * kD) + at;
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) {
+            float v[16];
+#pragma unroll
+            for (int x = 0; x < 16; x += 4) {
+                const float4 f = src ? *reinterpret_cast<const float4 *>(src + c + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[x] = f.x; v[x + 1] = f.y; v[x + 2] = f.z; v[x + 3] = f.w;
+            }
+            tmem_st16(trow + TM_S + c, v);
+            if (kDump && w.nch > 0) draw(c, v);
+        }
+        tmem_wait_st();
+        if (kDump && w.nch > 0) store_image(0);
+        const float dec_full = exp2f(l2 * (float)kC);
         bool ok = true;
         for (int it = 0; it < w.nch; ++it) {
-            if (kDump) {
-                if (tid == 0) bulk_wait_read_all();  // the image buffer is free again
-                state_barrier();
-#pragma unroll
-                for (int x = 0; x < 32; x += 8) {
-                    const uint4 v = make_uint4(pack_bf16(S[x], S[x + 1]), pack_bf16(S[x + 2], S[x + 3]),
-                                               pack_bf16(S[x + 4], S[x + 5]), pack_bf16(S[x + 6], S[x + 7]));
-                    *reinterpret_cast<uint4 *>(image + sw128(row, 64 * (cg & 1) + 2 * x)) = v;
-                }
-                fence_proxy_async_smem();
-                state_barrier();
-                if (tid == 0) {
-                    const int64_t cs = chunk0 + w.chunk(it);
-                    bulk_store(p.dump + (cs * p.H + h) * (int64_t)kTile, sm + OFF_IMAGE, kTile);
-                    bulk_commit();
-                }
-            }
-            // every warp goes on after a wait given up, so that the barriers above stay whole
+            // every warp goes on after a wait given up, so that the barriers stay whole
             if (ok) ok = role_wait(&ms->sum_full[it & 1], (it >> 1) & 1, &ms->abort, p.err);
             tc_fence_after_sync();
+            const bool more = kDump && it + 1 < w.nch;
+            if (more) {
+                if (tid == 0) bulk_wait_read_all();  // the image buffer is free again
+                state_barrier();
+            }
             const int L = w.length(it);
             const float dec = L < kC ? exp2f(l2 * (float)L) : dec_full;
-            float d[32];
-            tmem_ld32(trow + 128 * (it & 1), d);
-            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) {
+                float v[16], d[16];
+                tmem_ld16(trow + TM_S + c, v);
+                tmem_ld16(trow + 128 * (it & 1) + c, d);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 16; ++x) v[x] = fmaf(dec, v[x], d[x]);
+                tmem_st16(trow + TM_S + c, v);
+                if (more) draw(c, v);
+            }
+            tmem_wait_st();
             tc_fence_before_sync();
             mbar_arrive(&ms->sum_empty[it & 1]);
-#pragma unroll
-            for (int x = 0; x < 32; ++x) S[x] = fmaf(dec, S[x], d[x]);
+            if (more) store_image(it + 1);
         }
         float *dst = kDump ? (last && p.mT && st >= 0 ? p.mT + (st * p.H + h) * (int64_t)(kD * kD) : nullptr)
                            : p.seg + (slot * p.H + h) * (int64_t)(kD * kD);
         if (ok && dst) {
 #pragma unroll
-            for (int x = 0; x < 32; x += 4)
-                *reinterpret_cast<float4 *>(dst + at + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
+            for (int c = 0; c < 64; c += 32) {
+                float v[32];
+                tmem_ld32(trow + TM_S + c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 32; x += 4)
+                    *reinterpret_cast<float4 *>(dst + at + c + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+            }
         }
         if (kDump && tid == 0) bulk_wait_all();
     }
@@ -296,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 0) tmem_dealloc(tmem, 256);
+    if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 template <bool kDump>

@@ -73,6 +73,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&t);
 }
+__device__ __forceinline__ uint32_t pack_bf16(float2 a) { return pack_bf16(a.x, a.y); }
 
 // Both 64-column halves of the 128-token tile of head h at token t0.
 __device__ __forceinline__ void load_tile(void *dst, const CUtensorMap *map, uint64_t *bar, int h, int64_t t0) {
@@ -80,12 +81,28 @@ __device__ __forceinline__ void load_tile(void *dst, const CUtensorMap *map, uin
     tma_load_3d(static_cast<uint8_t *>(dst) + kSub, map, bar, 64, h, (int32_t)t0);
 }
 
+// mbarrier wait that the hardware may hold for up to ~20 us: a waiting warp then
+// issues next to nothing (a plain polling loop took issue slots from the others).
+__device__ __forceinline__ bool mbar_try_wait_long(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Waits of the warp-specialised kernels: give up when another role has
 // (`abort`), or after kWaitLimit clocks, raising `abort` and the error flag.
 __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, volatile int32_t *abort, int32_t *err) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_long(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!mbar_try_wait_long(bar, parity)) {
         if (*abort) return false;
         if (clock64() - t0 > kWaitLimit) {
             *abort = 1;
@@ -94,6 +111,11 @@ __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, volati
         }
     }
     return true;
+}
+
+// Two bf16 of a word as floats.
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 // The states entering every chunk, found by one pass over a value-like array x
