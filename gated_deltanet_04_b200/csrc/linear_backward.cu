@@ -26,7 +26,7 @@ namespace gdn {
 namespace linear {
 namespace {
 
-constexpr int kEpiThreads = 256;
+constexpr int kEpiWarps = 8, kEpiThreads = 32 * kEpiWarps;
 constexpr int kThreads = kEpiThreads + 64;
 enum Buf { B_V0 = 0, B_V1, B_DO, B_K, B_S, B_Q, B_G, kBufs };
 constexpr uint32_t OFF_MISC = kBufs * kTile;
@@ -188,7 +188,7 @@ __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t 
     auto done = [&]() {
         tmem_wait_st();
         tc_fence_before_sync();
-        mbar_arrive(&ms->epi_done);
+        warp_arrive(&ms->epi_done);
     };
     // A0 = R times scale lam^|row - column| where the column is not after
     // (kLower) or not before the row, 0 elsewhere
@@ -277,7 +277,7 @@ __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t 
         if (!wait(ms->item_full[n & 1], n >> 1)) return;
         const Item im = ms->item[n & 1];
         if (im.L < 0) break;
-        mbar_arrive(&ms->item_empty[n & 1]);
+        warp_arrive(&ms->item_empty[n & 1]);
         for (int g = 0; g < G; ++g, ++u) {
             const int h = im.j * G + g, bv = u & 1 ? B_V1 : B_V0;
             const float l2 = p.log_decay[h] * kLog2e;
@@ -291,7 +291,7 @@ __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t 
                     clear(B_Q, im.L);
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(&ms->clean);
+                warp_arrive(&ms->clean);
             }
             __syncwarp();
             up[lane] = exp2f(l2 * (float)lane);
@@ -344,11 +344,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ms->item_full[b], 1);
-            mbar_init(&ms->item_empty[b], 1 + kEpiThreads);
+            mbar_init(&ms->item_empty[b], 1 + kEpiWarps);
         }
         mbar_init(&ms->mma_done, 1);
-        mbar_init(&ms->epi_done, kEpiThreads);
-        mbar_init(&ms->clean, kEpiThreads);
+        mbar_init(&ms->epi_done, kEpiWarps);
+        mbar_init(&ms->clean, kEpiWarps);
         mbar_init(&ms->drain, 1);
         ms->abort = 0;
         fence_mbarrier_init();

@@ -19,7 +19,7 @@ namespace gdn {
 namespace linear {
 namespace {
 
-constexpr int kEpiThreads = 256;
+constexpr int kEpiWarps = 8, kEpiThreads = 32 * kEpiWarps;
 constexpr int kThreads = kEpiThreads + 64;
 constexpr int kRing = 4;
 constexpr uint32_t OFF_Q = 0, OFF_K = 2 * kTile, OFF_RING = 3 * kTile, OFF_MISC = OFF_RING + kRing * kTile;
@@ -189,7 +189,7 @@ __device__ void epilogue(const OutPass &p, uint8_t *sm, Misc *ms, uint32_t tmem,
         }
         tmem_wait_ld();
         tc_fence_before_sync();
-        mbar_arrive(&ms->o_free);
+        warp_arrive(&ms->o_free);
         if (i >= L) return true;
         const float f = p.scale * exp2f(l2 * (float)(i + 1));
         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.o) + ((t0 + i) * p.Hv + h) * (int64_t)kD + 64 * half;
@@ -212,7 +212,7 @@ __device__ void epilogue(const OutPass &p, uint8_t *sm, Misc *ms, uint32_t tmem,
         if (!wait(ms->full_q[n & 1], n >> 1)) return;
         const Item im = ms->item[n & 1];
         if (im.L < 0) break;
-        mbar_arrive(&ms->empty_q[n & 1]);
+        warp_arrive(&ms->empty_q[n & 1]);
         if (!wait(ms->qk_done, n)) return;
         tc_fence_after_sync();
         for (int g = 0; g < G; ++g, ++u, r += 2) {
@@ -229,8 +229,8 @@ __device__ void epilogue(const OutPass &p, uint8_t *sm, Misc *ms, uint32_t tmem,
             }
             make_p(u, l2);
             tc_fence_before_sync();
-            mbar_arrive(&ms->p_ready[u & 1]);
-            if (g == G - 1) mbar_arrive(&ms->qk_free);
+            warp_arrive(&ms->p_ready[u & 1]);
+            if (g == G - 1) warp_arrive(&ms->qk_free);
             if (prev_h >= 0 && !write_o(u - 1, prev_t0, prev_L, prev_h, prev_l2)) return;
             prev_t0 = im.t0;
             prev_L = im.L;
@@ -253,8 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ms->full_q[b], 1);
-            mbar_init(&ms->empty_q[b], 1 + kEpiThreads);
-            mbar_init(&ms->p_ready[b], kEpiThreads);
+            mbar_init(&ms->empty_q[b], 1 + kEpiWarps);
+            mbar_init(&ms->p_ready[b], kEpiWarps);
         }
         mbar_init(&ms->full_k, 1);
         mbar_init(&ms->empty_k, 1);
@@ -264,9 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&ms->drain, 1);
         mbar_init(&ms->qk_done, 1);
-        mbar_init(&ms->qk_free, kEpiThreads);
+        mbar_init(&ms->qk_free, kEpiWarps);
         mbar_init(&ms->o_done, 1);
-        mbar_init(&ms->o_free, kEpiThreads);
+        mbar_init(&ms->o_free, kEpiWarps);
         ms->abort = 0;
         fence_mbarrier_init();
     }

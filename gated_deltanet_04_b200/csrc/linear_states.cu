@@ -11,12 +11,14 @@
 // passes, wherever the sum goes into an fp32 state.  Where only bf16 images
 // come of it (a segment that does not end its sequence), hi + mid do.
 //
-// Roles, on stages of 64 tokens: a producer warp loads x and y by TMA into a
-// ring; two groups of 8 warps take stages in turn, turning x in place into hi
-// and writing mid and lo beside it (one group alone was bound by the latency of
-// its steps, 2.2 us a chunk with or without lo); an MMA warp sums a chunk's
-// stages into one of two accumulators; 8 warps add it to the state and store
-// the image of the state that enters the next chunk.
+// Shared memory bandwidth bounds this kernel (128 B a clock; the products alone
+// read 64 KB per part, chunk and head), so x does not pass through it on its
+// way in: the converting warps load it from global memory, a stage ahead.
+//
+// Roles, on stages of 64 tokens: a producer warp loads y by TMA into a ring; 16
+// warps write x's parts into two buffers in turn; an MMA warp sums a chunk's
+// stages into one of two accumulators; 8 warps add it to the state and store the
+// image of the state that enters the next chunk.
 // Bound: HBM (64 KB in, 32 KB image out per chunk and head, y shared by the
 // heads of a group through L2) against two or three products of 4.2 MFLOP.
 #include "linear_tc.cuh"
@@ -28,13 +30,13 @@ namespace {
 constexpr int kRows = 64;                    // tokens per stage
 constexpr uint32_t kHalf = kRows * 128;      // 64 rows x 64 columns
 constexpr uint32_t kPart = 2 * kHalf;        // 64 x 128 bf16
-constexpr int kRing = 4;
-constexpr int kStateWarps = 8, kConvWarps = 8, kConvGroups = 2;
+constexpr int kRing = 6;                     // stages of y
+constexpr int kStateWarps = 8, kConvWarps = 16;
 constexpr int kStateThreads = kStateWarps * 32, kConvThreads = kConvWarps * 32;
-constexpr int kThreads = kStateThreads + kConvGroups * kConvThreads + 64;
-constexpr uint32_t TM_S = 256;  // tensor memory: two sums, the state
-constexpr uint32_t OFF_PARTS = kRing * 2 * kPart;       // [2][mid, lo]
-constexpr uint32_t OFF_IMAGE = OFF_PARTS + 4 * kPart;
+constexpr int kThreads = kStateThreads + kConvThreads + 64;
+constexpr uint32_t TM_S = 256;               // tensor memory: two sums, the state
+constexpr uint32_t OFF_PARTS = kRing * kPart;           // [2][hi, mid, lo]
+constexpr uint32_t OFF_IMAGE = OFF_PARTS + 6 * kPart;
 constexpr uint32_t OFF_MISC = OFF_IMAGE + kTile;
 
 struct Misc {
@@ -45,21 +47,16 @@ struct Misc {
 constexpr uint32_t kSmem = OFF_MISC + sizeof(Misc) + 1024;
 static_assert(kSmem <= 232448, "shared memory of an SM");
 
-// The chunks of a segment in the pass's order.
+// The chunks of a segment in the pass's order: tokens t0 .. t0 + len - 1.
 struct Walk {
-    int64_t t0, t1;
-    int nch;
+    int64_t t0;
+    int32_t len, nch;
     bool reverse;
     __device__ __forceinline__ int chunk(int it) const { return reverse ? nch - 1 - it : it; }
-    __device__ __forceinline__ int64_t start(int it) const { return t0 + (int64_t)chunk(it) * kC; }
-    __device__ __forceinline__ int length(int it) const {
-        const int64_t left = t1 - start(it);
-        return left < kC ? (int)left : kC;
-    }
+    __device__ __forceinline__ int length(int it) const { return min(len - chunk(it) * kC, kC); }
 };
 
-__device__ void produce(const CUtensorMap &tm_x, const CUtensorMap &tm_y, const Walk &w, int h, int hy, uint8_t *sm,
-                        Misc *ms, int32_t *err) {
+__device__ void produce(const CUtensorMap &tm_y, const Walk &w, int hy, uint8_t *sm, Misc *ms, int32_t *err) {
     uint32_t r = 0;  // stages so far
     for (int it = 0; it < w.nch; ++it) {
         const int L = w.length(it);
@@ -71,97 +68,147 @@ __device__ void produce(const CUtensorMap &tm_x, const CUtensorMap &tm_y, const 
                     mbar_wait_bounded(&ms->raw_full[x % kRing], (x / kRing) & 1, kWaitLimit);
                 return;
             }
-            uint8_t *y = sm + b * 2 * kPart, *x = y + kPart;
-            const int32_t t = (int32_t)(w.start(it) + j0);
-            mbar_arrive_expect_tx(&ms->raw_full[b], 2 * kPart);
-            tma_load_3d(x, &tm_x, &ms->raw_full[b], 0, h, t);
-            tma_load_3d(x + kHalf, &tm_x, &ms->raw_full[b], 64, h, t);
+            uint8_t *y = sm + b * kPart;
+            const int32_t t = (int32_t)w.t0 + w.chunk(it) * kC + j0;
+            mbar_arrive_expect_tx(&ms->raw_full[b], kPart);
             tma_load_3d(y, &tm_y, &ms->raw_full[b], 0, hy, t);
             tma_load_3d(y + kHalf, &tm_y, &ms->raw_full[b], 64, hy, t);
         }
     }
 }
 
-// x w = hi + mid + lo: hi in place, the others into the parts buffer of the
-// group, which takes every second stage.
-__device__ void convert(const Walk &w, float l2, float x_scale, int parts, uint8_t *sm, Misc *ms, int group, int tid,
-                        int32_t *err) {
-    const int r0 = tid >> 3, piece = (tid & 7) * 16;  // rows r0 and r0 + 32 of a stage
-    const float2 minus = make_float2(-1.f, -1.f);
-    uint32_t r = 0;  // stages so far, of both groups
+// A weight in three bf16 parts (24 bits), each twice in a word.
+struct Weight {
+    uint32_t h, m, l;
+};
+__device__ __forceinline__ uint32_t twice_bf16(float x) { return pack_bf16(x, x); }
+__device__ __forceinline__ Weight split_weight(float w) {
+    Weight f;
+    f.h = twice_bf16(w);
+    const float r = w - unpack_bf16(f.h).x;
+    f.m = twice_bf16(r);
+    f.l = twice_bf16(r - unpack_bf16(f.m).x);
+    return f;
+}
+
+// Packed bf16 pairs: fused multiply-add, product, difference, one rounding each.
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    return fma2(a, b, 0x80008000u);  // - 0: keeps the sign of a zero product
+}
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) { return fma2(b, 0xbf80bf80u, a); }  // a - b
+
+// x w = hi + mid + lo, stage after stage into the two parts buffers in turn, in
+// packed bf16 arithmetic (fused multiply-adds, one rounding each): hi = x wh
+// rounded; x wh - hi is exact (16 bits less the upper 8), so mid = x wm + (x wh -
+// hi) is rounded once, and lo takes what mid's rounding left and x wl.
+// x: head h's row of token 0, `stride` elements from token to token.
+template <int kParts>
+__device__ void convert(const Walk &w, const __nv_bfloat16 *x, int64_t stride, float l2, float x_scale, uint8_t *sm,
+                        Misc *ms, int tid, int32_t *err) {
+    const int r0 = tid >> 4, col = (tid & 15) * 8;  // rows r0 and r0 + 32 of a stage, 8 columns from col
+    const uint32_t at = (col >> 6) * kHalf + sw128(r0, (col & 63) * 2);  // row r0 + 32: 4096 further
     // weight of row j of a chunk of L tokens (0 past its end)
     auto weight = [&](int j, int L) {
         if (j >= L) return 0.f;
         return w.reverse ? x_scale * exp2f(l2 * (float)(j + 1)) : exp2f(l2 * (float)(L - 1 - j));
     };
-    float wfull[4];  // of whole chunks
+    // a thread's share of a stage: rows r0 and r0 + 32; weights of a whole chunk's stages
+    const Weight whole[2][2] = {{split_weight(weight(r0, kC)), split_weight(weight(r0 + 32, kC))},
+                                {split_weight(weight(r0 + 64, kC)), split_weight(weight(r0 + 96, kC))}};
+    uint4 v[2][2];  // x of the next chunk's stages
+    auto load = [&](int it, int s) {
+        if (it >= w.nch) return;
+        const int c = w.chunk(it), left = w.len - c * kC - s * kRows - r0;
+        const __nv_bfloat16 *src = x + (w.t0 + c * kC + s * kRows + r0) * stride + col;
+        v[s][0] = left > 0 ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0u, 0u, 0u, 0u);
+        v[s][1] = left > 32 ? __ldg(reinterpret_cast<const uint4 *>(src + 32 * stride)) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint32_t r = 0;
+    auto piece = [&](const uint4 &x4, const Weight &f, uint8_t *dst) {
+        const uint32_t in[4] = {x4.x, x4.y, x4.z, x4.w};
+        uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wfull[i] = weight(r0 + 32 * i, kC);
+        for (int q = 0; q < 4; ++q) {
+            hi[q] = mul2(in[q], f.h);
+            const uint32_t rest = fma2(in[q], f.h, hi[q] ^ 0x80008000u);
+            mid[q] = fma2(in[q], f.m, rest);
+            if (kParts == 3) lo[q] = fma2(in[q], f.l, fma2(in[q], f.m, sub2(rest, mid[q])));
+        }
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(dst + kPart) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+        if (kParts == 3) *reinterpret_cast<uint4 *>(dst + 2 * kPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    };
+    load(0, 0);
+    load(0, 1);
     for (int it = 0; it < w.nch; ++it) {
         const int L = w.length(it);
-        for (int s = 0; s * kRows < L; ++s, ++r) {
-            if ((r & 1) != group) continue;
-            const int b = r % kRing;
-            if (!role_wait(&ms->raw_full[b], (r / kRing) & 1, &ms->abort, err)) return;
-            if (r >= 2 && !role_wait(&ms->part_empty[r & 1], ((r >> 1) - 1) & 1, &ms->abort, err)) return;
-            uint8_t *y = sm + b * 2 * kPart, *x = y + kPart, *mid = sm + OFF_PARTS + (r & 1) * 2 * kPart;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int j = s * kRows + r0 + 32 * i;
-                const float f = L == kC ? (s ? wfull[2 + i] : wfull[i]) : weight(j, L);
-#pragma unroll
-                for (int sub = 0; sub < 2; ++sub) {
-                    const uint32_t at = sub * kHalf + (r0 + 32 * i) * 128 + piece;
-                    uint32_t a[4] = {0u, 0u, 0u, 0u}, m[4] = {0u, 0u, 0u, 0u}, l[4] = {0u, 0u, 0u, 0u};
-                    if (j < L) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(x + at);
-                        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const float2 e = fmul2(unpack_bf16(in[q]), make_float2(f, f));
-                            a[q] = pack_bf16(e);
-                            const float2 d = ffma2(unpack_bf16(a[q]), minus, e);
-                            m[q] = pack_bf16(d);
-                            if (parts == 3) l[q] = pack_bf16(ffma2(unpack_bf16(m[q]), minus, d));
-                        }
-                    } else {  // rows of the next sequence: y too, or its NaN would reach this sum
-                        *reinterpret_cast<uint4 *>(y + at) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    *reinterpret_cast<uint4 *>(x + at) = make_uint4(a[0], a[1], a[2], a[3]);
-                    *reinterpret_cast<uint4 *>(mid + at) = make_uint4(m[0], m[1], m[2], m[3]);
-                    if (parts == 3) *reinterpret_cast<uint4 *>(mid + kPart + at) = make_uint4(l[0], l[1], l[2], l[3]);
-                }
+        for (int s = 0; s < 2; ++s) {
+            if (s * kRows >= L) {  // a short chunk's second stage
+                load(it + 1, s);
+                continue;
+            }
+            const int buf = r & 1, left = L - s * kRows;
+            if (r >= 2 && !role_wait(&ms->part_empty[buf], ((r >> 1) - 1) & 1, &ms->abort, err)) return;
+            uint8_t *dst = sm + OFF_PARTS + buf * 3 * kPart + at;
+            if (L == kC) {
+                piece(v[s][0], whole[s][0], dst);
+                piece(v[s][1], whole[s][1], dst + 4096);
+            } else {
+                piece(v[s][0], split_weight(weight(s * kRows + r0, L)), dst);
+                piece(v[s][1], split_weight(weight(s * kRows + r0 + 32, L)), dst + 4096);
+            }
+            load(it + 1, s);
+            if (left < kRows) {  // rows of the next sequence: 0 times their NaN would reach this sum
+                const int b = r % kRing;
+                if (!role_wait(&ms->raw_full[b], (r / kRing) & 1, &ms->abort, err)) return;
+                for (int k = tid; k < (kRows - left) * 16; k += kConvThreads)
+                    *reinterpret_cast<uint4 *>(sm + b * kPart + (k & 1) * kHalf + left * 128 + (k >> 1) * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
-            mbar_arrive(&ms->part_full[r & 1]);
+            warp_arrive(&ms->part_full[buf]);
+            ++r;
         }
     }
 }
 
-// D (+)= x^T y over a stage's 64 tokens, both MN-major.
-__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t x, uint32_t y, bool acc) {
-#pragma unroll
-    for (int ks = 0; ks < kRows / 16; ++ks)
-        mma_f16_ss(d, make_sdesc(x + ks * 2048, kHalf, 1024), make_sdesc(y + ks * 2048, kHalf, 1024), IDESC_MM,
-                   acc || ks);
-}
-
-__device__ void multiply(const Walk &w, int parts, uint32_t sbase, uint32_t tmem, Misc *ms, int32_t *err) {
-    uint32_t r = 0;
+// Sums a chunk's stages: D = (hi + mid + lo)^T y, both operands MN-major.
+template <int kParts>
+__device__ void multiply(const Walk &w, uint32_t sbase, uint32_t tmem, Misc *ms, int32_t *err) {
+    uint32_t r = 0, b = 0, lap = 0;  // stages so far; the ring's stage and lap
+    const uint64_t y0 = desc_m(sbase, kHalf), x0 = desc_m(sbase + OFF_PARTS, kHalf);
     bool ok = true;
     for (int it = 0; ok && it < w.nch; ++it) {
         const int L = w.length(it);
         const uint32_t d = tmem + 128 * (it & 1);
         if (it >= 2 && !(ok = role_wait(&ms->sum_empty[it & 1], ((it >> 1) - 1) & 1, &ms->abort, err))) break;
-        for (int j0 = 0; j0 < L; j0 += kRows, ++r) {
-            if (!(ok = role_wait(&ms->part_full[r & 1], (r >> 1) & 1, &ms->abort, err))) break;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (s * kRows >= L) break;
+            const uint32_t buf = r & 1;
+            if (!(ok = role_wait(&ms->raw_full[b], lap & 1, &ms->abort, err) &&
+                       role_wait(&ms->part_full[buf], (r >> 1) & 1, &ms->abort, err)))
+                break;
             tc_fence_after_sync();
-            const uint32_t y = sbase + (r % kRing) * 2 * kPart, mid = sbase + OFF_PARTS + (r & 1) * 2 * kPart;
-            mma_stage(d, y + kPart, y, j0 > 0);
-            mma_stage(d, mid, y, true);
-            if (parts == 3) mma_stage(d, mid + kPart, y, true);
-            mma_commit(&ms->raw_empty[r % kRing]);
-            mma_commit(&ms->part_empty[r & 1]);
+            const uint64_t y = y0 + b * (kPart >> 4), x = x0 + buf * (3 * kPart >> 4);
+#pragma unroll
+            for (int k = 0; k < kParts; ++k)
+#pragma unroll
+                for (int ks = 0; ks < kRows / 16; ++ks)
+                    mma_f16_ss(d, step_m(x + (k * kPart >> 4), ks), step_m(y, ks), IDESC_MM, s || k || ks);
+            mma_commit(&ms->raw_empty[b]);
+            mma_commit(&ms->part_empty[buf]);
+            ++r;
+            if (++b == kRing) {
+                b = 0;
+                ++lap;
+            }
         }
         if (ok) mma_commit(&ms->sum_full[it & 1]);
     }
@@ -178,8 +225,7 @@ __device__ __forceinline__ void state_barrier() {
 // kDump: the pass proper (images, final state); otherwise the segments' sums.
 template <bool kDump>
 __global__ void __launch_bounds__(kThreads, 1)
-    gdn_linear_states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
-                             StatePass p) {
+    gdn_linear_states_kernel(const __grid_constant__ CUtensorMap tm_y, StatePass p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Misc *ms = reinterpret_cast<Misc *>(sm + OFF_MISC);
@@ -193,9 +239,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool last = p.reverse ? sp.s == 0 : sp.s == sp.count - 1;  // in the pass's order
     if (!kDump && last) return;  // nothing starts from its sum
     const int hy = h / (p.H / p.Hy);
-    const Walk w{sp.t0, sp.t1, (int)((sp.t1 - sp.t0 + kC - 1) / kC), p.reverse};
+    const int32_t len = (int32_t)(sp.t1 - sp.t0);
+    const Walk w{sp.t0, len, (len + kC - 1) / kC, p.reverse};
     const float l2 = p.log_decay[h] * kLog2e;
-    const int parts = kDump && !(last && p.mT) ? 2 : 3;
+    const bool exact = !kDump || (last && p.mT);  // its sum goes into an fp32 state
 
     if (tid == 0) {
         for (int b = 0; b < kRing; ++b) {
@@ -203,10 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ms->raw_empty[b], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&ms->part_full[b], kConvThreads);
+            mbar_init(&ms->part_full[b], kConvWarps);
             mbar_init(&ms->part_empty[b], 1);
             mbar_init(&ms->sum_full[b], 1);
-            mbar_init(&ms->sum_empty[b], kStateThreads);
+            mbar_init(&ms->sum_empty[b], kStateWarps);
         }
         mbar_init(&ms->drain, 1);
         ms->abort = 0;
@@ -223,12 +270,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kStateWarps) {
         const int cw = warp - kStateWarps;
-        if (cw < kConvGroups * kConvWarps)
-            convert(w, l2, p.x_scale, parts, sm, ms, cw / kConvWarps, (tid - kStateThreads) % kConvThreads, p.err);
-        else if (cw == kConvGroups * kConvWarps) {
-            if (lane == 0) produce(tm_x, tm_y, w, h, hy, sm, ms, p.err);
+        if (cw < kConvWarps) {
+            const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)h * kD;
+            if (exact) convert<3>(w, x, (int64_t)p.H * kD, l2, p.x_scale, sm, ms, tid - kStateThreads, p.err);
+            else convert<2>(w, x, (int64_t)p.H * kD, l2, p.x_scale, sm, ms, tid - kStateThreads, p.err);
+        } else if (cw == kConvWarps) {
+            if (lane == 0) produce(tm_y, w, hy, sm, ms, p.err);
         } else if (lane == 0) {
-            multiply(w, parts, smem_u32(sm), tmem, ms, p.err);
+            if (exact) multiply<3>(w, smem_u32(sm), tmem, ms, p.err);
+            else multiply<2>(w, smem_u32(sm), tmem, ms, p.err);
         }
     } else {
         const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;  // columns 64 half .. of row
@@ -297,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_wait_st();
             tc_fence_before_sync();
-            mbar_arrive(&ms->sum_empty[it & 1]);
+            warp_arrive(&ms->sum_empty[it & 1]);
             if (more) store_image(it + 1);
         }
         float *dst = kDump ? (last && p.mT && st >= 0 ? p.mT + (st * p.H + h) * (int64_t)(kD * kD) : nullptr)
@@ -323,14 +373,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kDump>
-cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &my, const StatePass &p, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap &my, const StatePass &p, cudaStream_t s) {
     const int64_t len = p.seg ? p.seg_chunks * kC : (p.T > 0 ? p.T : 1);
     const int64_t blocks = slots_of(p.T, p.N, len) * p.H;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(gdn_linear_states_kernel<kDump>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    gdn_linear_states_kernel<kDump><<<(unsigned)blocks, kThreads, kSmem, s>>>(mx, my, p);
+    gdn_linear_states_kernel<kDump><<<(unsigned)blocks, kThreads, kSmem, s>>>(my, p);
     return cudaGetLastError();
 }
 
@@ -365,12 +415,11 @@ size_t state_seg_bytes(int32_t N, int64_t T, int32_t H) {
 size_t state_dump_bytes(int32_t N, int64_t T, int32_t H) { return (size_t)slots_of(T, N, kC) * H * kTile; }
 
 cudaError_t launch_states(const StatePass &p, cudaStream_t s) {
-    CUtensorMap mx, my;
+    CUtensorMap my;
     const int64_t Tm = p.T > 0 ? p.T : 1;
-    if (!make_tile_map_bf16_128(&mx, p.x, Tm, p.H, kRows) || !make_tile_map_bf16_128(&my, p.y, Tm, p.Hy, kRows))
-        return cudaErrorInvalidValue;
+    if (!make_tile_map_bf16_128(&my, p.y, Tm, p.Hy, kRows)) return cudaErrorInvalidValue;
     if (p.seg) {
-        cudaError_t e = launch<false>(mx, my, p, s);
+        cudaError_t e = launch<false>(my, p, s);
         if (e != cudaSuccess) return e;
         Pass scan{};
         scan.H = p.H; scan.Da = kD; scan.Dc = kD; scan.log_decay = p.log_decay; scan.reverse = p.reverse;
@@ -379,7 +428,7 @@ cudaError_t launch_states(const StatePass &p, cudaStream_t s) {
         e = launch_scan(scan, s);
         if (e != cudaSuccess) return e;
     }
-    return launch<true>(mx, my, p, s);
+    return launch<true>(my, p, s);
 }
 
 }  // namespace linear

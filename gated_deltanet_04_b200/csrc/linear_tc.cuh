@@ -29,37 +29,37 @@ constexpr uint32_t IDESC_KK = make_idesc_f16(128, 128, 0, 0, 1);
 constexpr uint32_t IDESC_KM = make_idesc_f16(128, 128, 0, 1, 1);
 constexpr uint32_t IDESC_MM = make_idesc_f16(128, 128, 1, 1, 1);
 
-// Descriptor of step ks (16 of the 128 summed elements) of a tile stored
-// [128 rows][128 columns]: rows are the operand's M (or N) index and columns the
-// summed one, or the other way round.
-__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int ks) {
-    return make_sdesc(tile + (ks >> 2) * kSub + (ks & 3) * 32, 16, 1024);
+// Descriptors of a tile stored [128 rows][128 columns]: rows are the operand's M
+// (or N) index and columns the summed one (K-major), or the other way round
+// (MN-major, `sub` bytes between its 64-column halves).  Step ks, 16 of the
+// summed elements, is a constant further in the address field, which is all that
+// an MMA's one issuing thread has to add (building each descriptor anew took it
+// longer than the tensor core took for the product).
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile) { return make_sdesc(tile, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_m(uint32_t tile, uint32_t sub = kSub) {
+    return make_sdesc(tile, sub, 1024);
 }
-__device__ __forceinline__ uint64_t desc_m(uint32_t tile, int ks) {
-    return make_sdesc(tile + ks * 2048, kSub, 1024);
+__device__ __forceinline__ uint64_t step_k(uint64_t d, int ks) {
+    return d + (uint64_t)(((ks >> 2) * kSub + (ks & 3) * 32) >> 4);
 }
+__device__ __forceinline__ uint64_t step_m(uint64_t d, int ks) { return d + (uint64_t)(ks * 2048 >> 4); }
 
-// D (+)= A B over 128 summed elements, operands in shared memory.
+// D (+)= A B over 128 summed elements, operands in shared memory; letters as above.
 __device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t b, bool acc) {
+    const uint64_t da = desc_k(a), db = desc_k(b);
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks) mma_f16_ss(d, desc_k(a, ks), desc_k(b, ks), IDESC_KK, acc || ks);
-}
-__device__ __forceinline__ void mma_km(uint32_t d, uint32_t a, uint32_t b, bool acc) {
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) mma_f16_ss(d, desc_k(a, ks), desc_m(b, ks), IDESC_KM, acc || ks);
-}
-__device__ __forceinline__ void mma_mm(uint32_t d, uint32_t a, uint32_t b, bool acc) {
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) mma_f16_ss(d, desc_m(a, ks), desc_m(b, ks), IDESC_MM, acc || ks);
+    for (int ks = 0; ks < 8; ++ks) mma_f16_ss(d, step_k(da, ks), step_k(db, ks), IDESC_KK, acc || ks);
 }
 // A from tensor memory (K-major, 64 columns of packed pairs), B MN-major or K-major.
 __device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a_tmem, uint32_t b, bool acc) {
+    const uint64_t db = desc_m(b);
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks) mma_f16_ts(d, a_tmem + 8 * ks, desc_m(b, ks), IDESC_KM, acc || ks);
+    for (int ks = 0; ks < 8; ++ks) mma_f16_ts(d, a_tmem + 8 * ks, step_m(db, ks), IDESC_KM, acc || ks);
 }
 __device__ __forceinline__ void mma_tk(uint32_t d, uint32_t a_tmem, uint32_t b, bool acc) {
+    const uint64_t db = desc_k(b);
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks) mma_f16_ts(d, a_tmem + 8 * ks, desc_k(b, ks), IDESC_KK, acc || ks);
+    for (int ks = 0; ks < 8; ++ks) mma_f16_ts(d, a_tmem + 8 * ks, step_k(db, ks), IDESC_KK, acc || ks);
 }
 
 // 32 bytes in one store: a whole memory sector per thread.
@@ -111,6 +111,13 @@ __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, volati
         }
     }
     return true;
+}
+
+// One arrival for a warp whose lanes have done their part (and fenced it).  32
+// lanes arriving one by one are 32 atomics on one word: half a chunk's time.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // Two bf16 of a word as floats.
