@@ -11,14 +11,16 @@
 // passes, wherever the sum goes into an fp32 state.  Where only bf16 images
 // come of it (a segment that does not end its sequence), hi + mid do.
 //
-// Shared memory bandwidth bounds this kernel (128 B a clock; the products alone
-// read 64 KB per part, chunk and head), so x does not pass through it on its
-// way in: the converting warps load it from global memory, a stage ahead.
+// The parts of x^T (128 rows, 64 tokens a stage) are the MMAs' first operand in
+// tensor memory, one row per lane: the converting threads load x from global
+// memory with a lane per column, which transposes it on the way.  (With both
+// operands in shared memory the products alone took all of its bandwidth, and
+// the kernel 2.6 us a chunk.)
 //
-// Roles, on stages of 64 tokens: a producer warp loads y by TMA into a ring; 16
-// warps write x's parts into two buffers in turn; an MMA warp sums a chunk's
-// stages into one of two accumulators; 8 warps add it to the state and store the
-// image of the state that enters the next chunk.
+// Roles, on stages of 64 tokens: a producer warp loads y by TMA into a ring; two
+// groups of 8 warps take stages in turn, each writing x's parts into a buffer of
+// its own; an MMA warp sums a chunk's stages into an accumulator; 8 warps add it to
+// the state and store the image of the state that enters the next chunk.
 // Bound: HBM (64 KB in, 32 KB image out per chunk and head, y shared by the
 // heads of a group through L2) against two or three products of 4.2 MFLOP.
 #include "linear_tc.cuh"
@@ -30,16 +32,26 @@ namespace {
 constexpr int kRows = 64;                    // tokens per stage
 constexpr uint32_t kHalf = kRows * 128;      // 64 rows x 64 columns
 constexpr uint32_t kPart = 2 * kHalf;        // 64 x 128 bf16
-constexpr int kRing = 6;                     // stages of y
-constexpr int kStateWarps = 8, kConvWarps = 16;
+constexpr int kRing = 8;                     // stages of y
+constexpr int kStateWarps = 8, kConvWarps = 16, kGroup = 8;  // warps; warps per converting group
 constexpr int kStateThreads = kStateWarps * 32, kConvThreads = kConvWarps * 32;
 constexpr int kThreads = kStateThreads + kConvThreads + 64;
-constexpr uint32_t TM_S = 256;               // tensor memory: two sums, the state
-constexpr uint32_t OFF_PARTS = kRing * kPart;           // [2][hi, mid, lo]
-constexpr uint32_t OFF_IMAGE = OFF_PARTS + 6 * kPart;
+constexpr uint32_t OFF_IMAGE = kRing * kPart;
 constexpr uint32_t OFF_MISC = OFF_IMAGE + kTile;
 
+// Tensor memory columns: the state, the sum; then with two parts a second sum
+// and two buffers of 2 x 32 columns, with three two buffers of 3 x 32.
+constexpr uint32_t TM_S = 0, TM_SUM = 128;
+template <int kParts>
+struct Columns {
+    static constexpr int kSums = kParts == 2 ? 2 : 1;
+    static constexpr uint32_t kFirst = TM_SUM + 128 * kSums;
+    static constexpr uint32_t parts(int buf) { return kFirst + buf * kParts * 32; }
+};
+static_assert(Columns<2>::parts(2) <= 512 && Columns<3>::parts(2) <= 512, "tensor memory");
+
 struct Misc {
+    alignas(16) uint32_t weight[2][3][kC / 2];  // of token pairs, in parts: a whole chunk's, the partial chunk's
     uint64_t raw_full[kRing], raw_empty[kRing], part_full[2], part_empty[2], sum_full[2], sum_empty[2], drain;
     uint32_t tmem;
     volatile int32_t abort;
@@ -77,20 +89,6 @@ __device__ void produce(const CUtensorMap &tm_y, const Walk &w, int hy, uint8_t 
     }
 }
 
-// A weight in three bf16 parts (24 bits), each twice in a word.
-struct Weight {
-    uint32_t h, m, l;
-};
-__device__ __forceinline__ uint32_t twice_bf16(float x) { return pack_bf16(x, x); }
-__device__ __forceinline__ Weight split_weight(float w) {
-    Weight f;
-    f.h = twice_bf16(w);
-    const float r = w - unpack_bf16(f.h).x;
-    f.m = twice_bf16(r);
-    f.l = twice_bf16(r - unpack_bf16(f.m).x);
-    return f;
-}
-
 // Packed bf16 pairs: fused multiply-add, product, difference, one rounding each.
 __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
@@ -102,92 +100,136 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) { return fma2(b, 0xbf80bf80u, a); }  // a - b
 
-// x w = hi + mid + lo, stage after stage into the two parts buffers in turn, in
-// packed bf16 arithmetic (fused multiply-adds, one rounding each): hi = x wh
-// rounded; x wh - hi is exact (16 bits less the upper 8), so mid = x wm + (x wh -
-// hi) is rounded once, and lo takes what mid's rounding left and x wl.
-// x: head h's row of token 0, `stride` elements from token to token.
-template <int kParts>
-__device__ void convert(const Walk &w, const __nv_bfloat16 *x, int64_t stride, float l2, float x_scale, uint8_t *sm,
-                        Misc *ms, int tid, int32_t *err) {
-    const int r0 = tid >> 4, col = (tid & 15) * 8;  // rows r0 and r0 + 32 of a stage, 8 columns from col
-    const uint32_t at = (col >> 6) * kHalf + sw128(r0, (col & 63) * 2);  // row r0 + 32: 4096 further
-    // weight of row j of a chunk of L tokens (0 past its end)
-    auto weight = [&](int j, int L) {
+// The weights of a chunk of L tokens (0 past its end) as bf16 parts hi + mid + lo
+// (24 bits) of pairs of tokens; thread i < 64 has pair i.
+__device__ __forceinline__ void make_weights(uint32_t (*dst)[kC / 2], int i, int L, bool reverse, float l2,
+                                             float x_scale) {
+    auto weight = [&](int j) {
         if (j >= L) return 0.f;
-        return w.reverse ? x_scale * exp2f(l2 * (float)(j + 1)) : exp2f(l2 * (float)(L - 1 - j));
+        return reverse ? x_scale * exp2f(l2 * (float)(j + 1)) : exp2f(l2 * (float)(L - 1 - j));
     };
-    // a thread's share of a stage: rows r0 and r0 + 32; weights of a whole chunk's stages
-    const Weight whole[2][2] = {{split_weight(weight(r0, kC)), split_weight(weight(r0 + 32, kC))},
-                                {split_weight(weight(r0 + 64, kC)), split_weight(weight(r0 + 96, kC))}};
-    uint4 v[2][2];  // x of the next chunk's stages
-    auto load = [&](int it, int s) {
-        if (it >= w.nch) return;
-        const int c = w.chunk(it), left = w.len - c * kC - s * kRows - r0;
-        const __nv_bfloat16 *src = x + (w.t0 + c * kC + s * kRows + r0) * stride + col;
-        v[s][0] = left > 0 ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0u, 0u, 0u, 0u);
-        v[s][1] = left > 32 ? __ldg(reinterpret_cast<const uint4 *>(src + 32 * stride)) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    uint32_t r = 0;
-    auto piece = [&](const uint4 &x4, const Weight &f, uint8_t *dst) {
-        const uint32_t in[4] = {x4.x, x4.y, x4.z, x4.w};
-        uint32_t hi[4], mid[4], lo[4];
+    float2 f = make_float2(weight(2 * i), weight(2 * i + 1));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            hi[q] = mul2(in[q], f.h);
-            const uint32_t rest = fma2(in[q], f.h, hi[q] ^ 0x80008000u);
-            mid[q] = fma2(in[q], f.m, rest);
-            if (kParts == 3) lo[q] = fma2(in[q], f.l, fma2(in[q], f.m, sub2(rest, mid[q])));
-        }
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(dst + kPart) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-        if (kParts == 3) *reinterpret_cast<uint4 *>(dst + 2 * kPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    };
-    load(0, 0);
-    load(0, 1);
-    for (int it = 0; it < w.nch; ++it) {
-        const int L = w.length(it);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (s * kRows >= L) {  // a short chunk's second stage
-                load(it + 1, s);
-                continue;
-            }
-            const int buf = r & 1, left = L - s * kRows;
-            if (r >= 2 && !role_wait(&ms->part_empty[buf], ((r >> 1) - 1) & 1, &ms->abort, err)) return;
-            uint8_t *dst = sm + OFF_PARTS + buf * 3 * kPart + at;
-            if (L == kC) {
-                piece(v[s][0], whole[s][0], dst);
-                piece(v[s][1], whole[s][1], dst + 4096);
-            } else {
-                piece(v[s][0], split_weight(weight(s * kRows + r0, L)), dst);
-                piece(v[s][1], split_weight(weight(s * kRows + r0 + 32, L)), dst + 4096);
-            }
-            load(it + 1, s);
-            if (left < kRows) {  // rows of the next sequence: 0 times their NaN would reach this sum
-                const int b = r % kRing;
-                if (!role_wait(&ms->raw_full[b], (r / kRing) & 1, &ms->abort, err)) return;
-                for (int k = tid; k < (kRows - left) * 16; k += kConvThreads)
-                    *reinterpret_cast<uint4 *>(sm + b * kPart + (k & 1) * kHalf + left * 128 + (k >> 1) * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            warp_arrive(&ms->part_full[buf]);
-            ++r;
-        }
+    for (int k = 0; k < 3; ++k) {
+        const uint32_t part = pack_bf16(f);
+        dst[k][i] = part;
+        const float2 g = unpack_bf16(part);
+        f = make_float2(f.x - g.x, f.y - g.y);
     }
 }
 
-// Sums a chunk's stages: D = (hi + mid + lo)^T y, both operands MN-major.
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Every second stage (group 0 or 1): x^T w = hi + mid + lo into tensor memory, a
+// thread per row (column of x) and 32 of the tokens, in packed bf16 arithmetic
+// (fused multiply-adds, one rounding each): hi = x wh rounded; x wh - hi is exact
+// (16 bits less the upper 8), so mid = x wm + (x wh - hi) is rounded once, and lo
+// takes what mid's rounding left and x wl.  A pair of lanes loads its two columns
+// of two tokens, a token each, and swaps halves.  x: this lane pair's columns of
+// token 0, `stride` elements from token to token.
+template <int kParts>
+__device__ void convert(const Walk &w, const __nv_bfloat16 *x, int64_t stride, uint8_t *sm, Misc *ms, uint32_t tlane,
+                        int group, int half, int tid, int32_t *err) {
+    struct At {  // stage s of chunk it
+        int it, s;
+    };
+    auto advance = [&](At a) -> At {  // two stages on
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (a.it >= w.nch) break;
+            if (a.s == 0 && w.length(a.it) > kRows) a.s = 1;
+            else a = {a.it + 1, 0};
+        }
+        return a;
+    };
+    const int odd = tid & 1;
+    const uint32_t swap = odd ? 0x3276u : 0x5410u;
+    uint32_t next[16];  // the group's next stage: tokens 2 q + odd, two columns
+    auto load = [&](const At &a) {
+        if (a.it >= w.nch) return;
+        const int j0 = a.s * kRows + 32 * half, left = w.length(a.it) - j0 - odd;
+        const __nv_bfloat16 *src = x + (w.t0 + w.chunk(a.it) * kC + j0 + odd) * stride;
+        const int64_t step = 2 * stride;
+        if (left >= 31) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) next[q] = __ldg(reinterpret_cast<const uint32_t *>(src + q * step));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                next[q] = 2 * q < left ? __ldg(reinterpret_cast<const uint32_t *>(src + q * step)) : 0u;
+        }
+    };
+    const uint32_t dst = tlane + Columns<kParts>::parts(group) + 16 * half;
+    At a{0, 0};
+    if (group == 1) a = w.length(0) > kRows ? At{0, 1} : At{1, 0};
+    load(a);
+    for (uint32_t r = group; a.it < w.nch; r += 2) {
+        const int L = w.length(a.it), left = L - a.s * kRows;
+        const uint32_t(*wt)[kC / 2] = ms->weight[L < kC];
+        const int at = a.s * (kRows / 2) + 16 * half;
+#pragma unroll
+        for (int q = 0; q < 16; ++q)  // this lane's column, two tokens
+            next[q] = __byte_perm(next[q], __shfl_xor_sync(0xffffffffu, next[q], 1), swap);
+#pragma unroll
+        for (int q0 = 0; q0 < 16; q0 += 8) {
+            uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+            for (int q = 0; q < 8; q += 4) {
+                const uint4 h4 = *reinterpret_cast<const uint4 *>(&wt[0][at + q0 + q]);
+                const uint4 m4 = *reinterpret_cast<const uint4 *>(&wt[1][at + q0 + q]);
+                const uint32_t wh[4] = {h4.x, h4.y, h4.z, h4.w}, wm[4] = {m4.x, m4.y, m4.z, m4.w};
+                uint32_t wl[4] = {0u, 0u, 0u, 0u};
+                if (kParts == 3) {
+                    const uint4 l4 = *reinterpret_cast<const uint4 *>(&wt[2][at + q0 + q]);
+                    wl[0] = l4.x; wl[1] = l4.y; wl[2] = l4.z; wl[3] = l4.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t v = next[q0 + q + e], h = mul2(v, wh[e]);
+                    const uint32_t rest = fma2(v, wh[e], h ^ 0x80008000u), m = fma2(v, wm[e], rest);
+                    hi[q + e] = h;
+                    mid[q + e] = m;
+                    if (kParts == 3) lo[q + e] = fma2(v, wl[e], fma2(v, wm[e], sub2(rest, m)));
+                }
+            }
+            // as late as can be: the MMAs of the other group's stage cover what follows
+            if (q0 == 0 && r >= 2 && !role_wait(&ms->part_empty[group], ((r >> 1) - 1) & 1, &ms->abort, err)) return;
+            tmem_st8u(dst + q0, hi);
+            tmem_st8u(dst + 32 + q0, mid);
+            if (kParts == 3) tmem_st8u(dst + 64 + q0, lo);
+        }
+        if (left < kRows) {  // y of the next sequence: 0 times its NaN would reach this sum
+            const int b = r % kRing;
+            if (!role_wait(&ms->raw_full[b], (r / kRing) & 1, &ms->abort, err)) return;
+            for (int k = tid; k < (kRows - left) * 16; k += 32 * kGroup)
+                *reinterpret_cast<uint4 *>(sm + b * kPart + (k & 1) * kHalf + left * 128 + (k >> 1) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        warp_arrive(&ms->part_full[group]);
+        a = advance(a);
+        load(a);
+    }
+}
+
+// Sums a chunk's stages: D = (hi + mid + lo)^T y, y MN-major.
 template <int kParts>
 __device__ void multiply(const Walk &w, uint32_t sbase, uint32_t tmem, Misc *ms, int32_t *err) {
     uint32_t r = 0, b = 0, lap = 0;  // stages so far; the ring's stage and lap
-    const uint64_t y0 = desc_m(sbase, kHalf), x0 = desc_m(sbase + OFF_PARTS, kHalf);
+    constexpr int kSums = Columns<kParts>::kSums;
+    const uint64_t y0 = desc_m(sbase, kHalf);
     bool ok = true;
     for (int it = 0; ok && it < w.nch; ++it) {
         const int L = w.length(it);
-        const uint32_t d = tmem + 128 * (it & 1);
-        if (it >= 2 && !(ok = role_wait(&ms->sum_empty[it & 1], ((it >> 1) - 1) & 1, &ms->abort, err))) break;
+        const int sum = it % kSums;
+        const uint32_t d = tmem + TM_SUM + 128 * sum;
+        if (it >= kSums && !(ok = role_wait(&ms->sum_empty[sum], (it / kSums - 1) & 1, &ms->abort, err))) break;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             if (s * kRows >= L) break;
@@ -196,12 +238,13 @@ __device__ void multiply(const Walk &w, uint32_t sbase, uint32_t tmem, Misc *ms,
                        role_wait(&ms->part_full[buf], (r >> 1) & 1, &ms->abort, err)))
                 break;
             tc_fence_after_sync();
-            const uint64_t y = y0 + b * (kPart >> 4), x = x0 + buf * (3 * kPart >> 4);
+            const uint64_t y = y0 + b * (kPart >> 4);
+            const uint32_t x = tmem + Columns<kParts>::parts(buf);
 #pragma unroll
             for (int k = 0; k < kParts; ++k)
 #pragma unroll
                 for (int ks = 0; ks < kRows / 16; ++ks)
-                    mma_f16_ss(d, step_m(x + (k * kPart >> 4), ks), step_m(y, ks), IDESC_MM, s || k || ks);
+                    mma_f16_ts(d, x + 32 * k + 8 * ks, step_m(y, ks), IDESC_KM, s || k || ks);
             mma_commit(&ms->raw_empty[b]);
             mma_commit(&ms->part_empty[buf]);
             ++r;
@@ -210,7 +253,7 @@ __device__ void multiply(const Walk &w, uint32_t sbase, uint32_t tmem, Misc *ms,
                 ++lap;
             }
         }
-        if (ok) mma_commit(&ms->sum_full[it & 1]);
+        if (ok) mma_commit(&ms->sum_full[sum]);
     }
     if (ok) return;
     // given up: let the MMAs in flight finish before tensor memory is freed
@@ -250,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ms->raw_empty[b], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&ms->part_full[b], kConvWarps);
+            mbar_init(&ms->part_full[b], kGroup);
             mbar_init(&ms->part_empty[b], 1);
             mbar_init(&ms->sum_full[b], 1);
             mbar_init(&ms->sum_empty[b], kStateWarps);
@@ -258,6 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&ms->drain, 1);
         ms->abort = 0;
         fence_mbarrier_init();
+    }
+    if (tid < kC / 2) {
+        make_weights(ms->weight[0], tid, kC, w.reverse, l2, p.x_scale);
+        make_weights(ms->weight[1], tid, w.len % kC, w.reverse, l2, p.x_scale);
     }
     if (warp == 0) {
         tmem_alloc(&ms->tmem, 512);
@@ -271,9 +318,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kStateWarps) {
         const int cw = warp - kStateWarps;
         if (cw < kConvWarps) {
-            const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)h * kD;
-            if (exact) convert<3>(w, x, (int64_t)p.H * kD, l2, p.x_scale, sm, ms, tid - kStateThreads, p.err);
-            else convert<2>(w, x, (int64_t)p.H * kD, l2, p.x_scale, sm, ms, tid - kStateThreads, p.err);
+            // warp % 4 is the quarter of the lanes a warp may write
+            const int quad = warp & 3, row = quad * 32 + lane, half = (cw >> 2) & 1, group = cw / kGroup;
+            const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)h * kD + (row & ~1);
+            const uint32_t tlane = tmem + ((uint32_t)(quad * 32) << 16);
+            if (w.nch > 0 && exact) convert<3>(w, x, (int64_t)p.H * kD, sm, ms, tlane, group, half, row + 128 * half, p.err);
+            else if (w.nch > 0) convert<2>(w, x, (int64_t)p.H * kD, sm, ms, tlane, group, half, row + 128 * half, p.err);
         } else if (cw == kConvWarps) {
             if (lane == 0) produce(tm_y, w, hy, sm, ms, p.err);
         } else if (lane == 0) {
@@ -322,10 +372,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         if (kDump && w.nch > 0) store_image(0);
         const float dec_full = exp2f(l2 * (float)kC);
+        const int sums = exact ? Columns<3>::kSums : Columns<2>::kSums;
         bool ok = true;
         for (int it = 0; it < w.nch; ++it) {
             // every warp goes on after a wait given up, so that the barriers stay whole
-            if (ok) ok = role_wait(&ms->sum_full[it & 1], (it >> 1) & 1, &ms->abort, p.err);
+            const int sum = it % sums;
+            if (ok) ok = role_wait(&ms->sum_full[sum], (it / sums) & 1, &ms->abort, p.err);
             tc_fence_after_sync();
             const bool more = kDump && it + 1 < w.nch;
             if (more) {
@@ -338,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 64; c += 16) {
                 float v[16], d[16];
                 tmem_ld16(trow + TM_S + c, v);
-                tmem_ld16(trow + 128 * (it & 1) + c, d);
+                tmem_ld16(trow + TM_SUM + 128 * sum + c, d);
                 tmem_wait_ld();
 #pragma unroll
                 for (int x = 0; x < 16; ++x) v[x] = fmaf(dec, v[x], d[x]);
@@ -347,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_wait_st();
             tc_fence_before_sync();
-            warp_arrive(&ms->sum_empty[it & 1]);
+            warp_arrive(&ms->sum_empty[sum]);
             if (more) store_image(it + 1);
         }
         float *dst = kDump ? (last && p.mT && st >= 0 ? p.mT + (st * p.H + h) * (int64_t)(kD * kD) : nullptr)

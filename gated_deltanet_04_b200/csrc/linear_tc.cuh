@@ -81,28 +81,14 @@ __device__ __forceinline__ void load_tile(void *dst, const CUtensorMap *map, uin
     tma_load_3d(static_cast<uint8_t *>(dst) + kSub, map, bar, 64, h, (int32_t)t0);
 }
 
-// mbarrier wait that the hardware may hold for up to ~20 us: a waiting warp then
-// issues next to nothing (a plain polling loop took issue slots from the others).
-__device__ __forceinline__ bool mbar_try_wait_long(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n"
-        ".reg .pred p;\n"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n"
-        "selp.u32 %0, 1, 0, p;\n"
-        "}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // Waits of the warp-specialised kernels: give up when another role has
 // (`abort`), or after kWaitLimit clocks, raising `abort` and the error flag.
+// (A suspend-time hint on the wait made the whole chunk-state kernel 10% slower:
+// the hardware wakes such a warp later.)
 __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, volatile int32_t *abort, int32_t *err) {
-    if (mbar_try_wait_long(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!mbar_try_wait_long(bar, parity)) {
+    while (!mbar_try_wait(bar, parity)) {
         if (*abort) return false;
         if (clock64() - t0 > kWaitLimit) {
             *abort = 1;
