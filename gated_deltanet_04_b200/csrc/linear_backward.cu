@@ -7,29 +7,34 @@
 // tensor-core accumulators that live through the group's heads.
 //
 // Every (chunk, q/k head) is an item; a persistent CTA per SM takes items in
-// turn.  A producer warp loads tiles, an MMA warp multiplies, 8 epilogue warps
-// turn products into the next operands.  Tensor memory: the accumulators of dq
-// and dk, one working accumulator R, and two bf16 operands A0, A1.  Per head:
-//     R = dO V^T       -> A0 = masked, decayed;  A1 = scale lam^{i+1} dO
-//     dq += A0 K + A1 S;           R = K Q^T   -> A0 masked, A1 = lam^{L-1-j} K
-//     R = A0 dO + A1 G^T           -> dv out;     A1 = lam^{L-1-j} V
-//     R = V dO^T                   -> A0 masked
-//     dk += A0 Q + A1 G
-// Each masked score, scaled row and state is rounded to bf16 (2^-8 of a term).
-// Shared memory holds one head's tiles (V twice, so that the next head's can
-// come while this one's is in use): 7 x 32 KB.
+// turn.  A producer warp loads tiles, an MMA warp multiplies, 16 epilogue warps
+// (a row's 32 columns per thread) work between the products.  Per v-head, with
+// two working accumulators T0, T1 in tensor memory beside those of dq and dk:
+//     T0 = K Q^T    -> P^T (decayed, masked, bf16) in T0's place
+//     T1 = K G^T    -> rows times lam^{L-1-j};  T1 += P^T dO   -> dv out
+//     T0 = dO V^T   -> P' (decayed, masked, bf16) to shared memory
+//     T1 = dO S     -> dq += rows times scale lam^{i+1};       dq += P' K
+//     T0 = V G      -> dk += rows times lam^{L-1-j};           dk += P'^T Q
+// The row factors are applied in fp32 to the products, so that a term carries
+// two bf16 roundings at most beside its inputs': of the score or of the state
+// (2^-8 each).  P' in shared memory serves as both P' and P'^T.  (A first version
+// with 8 epilogue warps, rounded scaled rows and P'^T as a ninth product spent
+// 20,300 clocks a head, 9,200 of them in the epilogue.)
+// Shared memory holds one head's tiles and P': 7 x 32 KB; the order of the
+// products frees V, dO, S and G early enough for the next head's to come.
 // Bound: HBM, 160 KB per chunk and v-head (V, dO, S, G, dv) and q, k, dq, dk per
-// group, against nine 128^3 products (38 MFLOP).
+// group, against eight 128^3 products (34 MFLOP).
 #include "linear_tc.cuh"
 
 namespace gdn {
 namespace linear {
 namespace {
 
-constexpr int kEpiWarps = 8, kEpiThreads = 32 * kEpiWarps;
+constexpr int kEpiWarps = 16, kEpiThreads = 32 * kEpiWarps;
 constexpr int kThreads = kEpiThreads + 64;
-enum Buf { B_V0 = 0, B_V1, B_DO, B_K, B_S, B_Q, B_G, kBufs };
-constexpr uint32_t OFF_MISC = kBufs * kTile;
+constexpr int kSteps = 6;  // products of a head that the epilogue works on
+enum Buf { B_V = 0, B_DO, B_K, B_S, B_Q, B_G, kBufs };
+constexpr uint32_t OFF_P = kBufs * kTile, OFF_MISC = OFF_P + kTile;
 
 struct Item {
     int64_t t0;
@@ -37,10 +42,10 @@ struct Item {
 };
 
 struct Misc {
-    float up[8][32];  // per epilogue warp: lam^0 .. lam^31 of its head
+    float up[2][4][32];  // per head (in turn) and lane quarter: lam^0 .. lam^31
     uint64_t full[kBufs], empty[kBufs];
     uint64_t item_full[2], item_empty[2];
-    uint64_t mma_done, epi_done, clean, drain;
+    uint64_t mma_done[kSteps], epi_done[kSteps], clean, drain;
     Item item[2];
     uint32_t tmem;
     volatile int32_t abort;
@@ -48,16 +53,16 @@ struct Misc {
 constexpr uint32_t kSmem = OFF_MISC + sizeof(Misc) + 1024;
 static_assert(kSmem <= 232448, "shared memory of an SM");
 
-constexpr uint32_t TM_DQ = 0, TM_DK = 128, TM_R = 256, TM_A0 = 384, TM_A1 = 448;
+constexpr uint32_t TM_DQ = 0, TM_DK = 128, TM_T0 = 256, TM_T1 = 384;
 
 struct Maps {
     CUtensorMap q, k, v, g;  // g: dO
 };
 
-// Tiles in the order of their first use.  n, u: items and v-heads so far.
+// Tiles, in the order in which the head before lets go of their buffers.
 __device__ void produce(const Maps &m, const BackwardPass &p, int64_t items, uint8_t *sm, Misc *ms, int G) {
     volatile int32_t *abort = &ms->abort;
-    uint32_t cnt[kBufs] = {0, 0, 0, 0, 0, 0, 0};  // loads issued into each buffer
+    uint32_t cnt[kBufs] = {0, 0, 0, 0, 0, 0};  // loads issued into each buffer
     bool ok = true;
     auto acquire = [&](int b) {
         if (ok && cnt[b] > 0) ok = role_wait(&ms->empty[b], (cnt[b] - 1) & 1, abort, p.err);
@@ -67,7 +72,7 @@ __device__ void produce(const Maps &m, const BackwardPass &p, int64_t items, uin
         }
         return ok;
     };
-    uint32_t n = 0, u = 0;
+    uint32_t n = 0;
     for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
         const int64_t slot = it / p.Hqk;
         const int j = (int)(it - slot * p.Hqk);
@@ -77,25 +82,23 @@ __device__ void produce(const Maps &m, const BackwardPass &p, int64_t items, uin
         ms->item[n & 1] = {sp.t0, (int32_t)(sp.t1 - sp.t0), j};
         mbar_arrive(&ms->item_full[n & 1]);
         ++n;
-        for (int g = 0; g < G && ok; ++g, ++u) {
-            const int h = j * G + g, bv = u & 1 ? B_V1 : B_V0;
+        for (int g = 0; g < G && ok; ++g) {
+            const int h = j * G + g;
             const int64_t img = (slot * p.Hv + h) * (int64_t)kTile;
-            if (!acquire(bv)) break;
-            load_tile(sm + bv * kTile, &m.v, &ms->full[bv], h, sp.t0);
-            if (!acquire(B_DO)) break;
-            load_tile(sm + B_DO * kTile, &m.g, &ms->full[B_DO], h, sp.t0);
             if (g == 0) {
                 if (!acquire(B_K)) break;
                 load_tile(sm + B_K * kTile, &m.k, &ms->full[B_K], j, sp.t0);
-            }
-            if (!acquire(B_S)) break;
-            bulk_load(sm + B_S * kTile, p.dump_s + img, kTile, &ms->full[B_S]);
-            if (g == 0) {
                 if (!acquire(B_Q)) break;
                 load_tile(sm + B_Q * kTile, &m.q, &ms->full[B_Q], j, sp.t0);
             }
+            if (!acquire(B_DO)) break;
+            load_tile(sm + B_DO * kTile, &m.g, &ms->full[B_DO], h, sp.t0);
+            if (!acquire(B_S)) break;
+            bulk_load(sm + B_S * kTile, p.dump_s + img, kTile, &ms->full[B_S]);
             if (!acquire(B_G)) break;
             bulk_load(sm + B_G * kTile, p.dump_g + img, kTile, &ms->full[B_G]);
+            if (!acquire(B_V)) break;
+            load_tile(sm + B_V * kTile, &m.v, &ms->full[B_V], h, sp.t0);
         }
     }
     if (ok && n >= 2) ok = role_wait(&ms->item_empty[n & 1], ((n >> 1) - 1) & 1, abort, p.err);
@@ -109,17 +112,18 @@ __device__ void produce(const Maps &m, const BackwardPass &p, int64_t items, uin
         if (cnt[b] > 0) mbar_wait_bounded(&ms->full[b], (cnt[b] - 1) & 1, kWaitLimit);
 }
 
-// Issues every MMA (one thread); steps: four per v-head, each ended by a commit
-// to mma_done and followed by the epilogue's epi_done.
+// Issues every MMA (one thread).  Product k of a head (0 .. 5) is handed to the
+// epilogue by a commit to mma_done[k], and comes back by epi_done[k]: a barrier for
+// each, because two products may be done before the first is waited for.
 __device__ void multiply(const BackwardPass &p, uint32_t sbase, Misc *ms, uint32_t tmem, int G) {
     volatile int32_t *abort = &ms->abort;
     auto wait = [&](uint64_t &bar, uint32_t parity) { return role_wait(&bar, parity & 1, abort, p.err); };
     auto tile = [&](int b) { return sbase + b * kTile; };
-    const uint32_t dq = tmem + TM_DQ, dk = tmem + TM_DK, R = tmem + TM_R, A0 = tmem + TM_A0, A1 = tmem + TM_A1;
-    uint32_t u = 0, step = 0, dirty = 0;  // v-heads, epilogue steps, partial-chunk heads so far
-    auto epi = [&]() {  // the epilogue's current step is done
-        const bool ok = wait(ms->epi_done, step);
-        ++step;
+    const uint32_t dq = tmem + TM_DQ, dk = tmem + TM_DK, T0 = tmem + TM_T0, T1 = tmem + TM_T1;
+    const uint32_t P = sbase + OFF_P;
+    uint32_t u = 0, dirty = 0;  // v-heads, partial-chunk heads so far
+    auto epi = [&](int k) {  // the epilogue is done with product k
+        const bool ok = wait(ms->epi_done[k], u);
         tc_fence_after_sync();
         return ok;
     };
@@ -127,41 +131,40 @@ __device__ void multiply(const BackwardPass &p, uint32_t sbase, Misc *ms, uint32
         if (!wait(ms->item_full[n & 1], n >> 1)) break;
         const int L = ms->item[n & 1].L;
         if (L < 0) {
-            if (n > 0) mma_commit(&ms->mma_done);  // the last item's dq and dk
+            if (n > 0) mma_commit(&ms->mma_done[0]);  // the last item's dq and dk
             return;
         }
         mbar_arrive(&ms->item_empty[n & 1]);
         bool ok = true;
         for (int g = 0; g < G; ++g, ++u) {
-            const int bv = u & 1 ? B_V1 : B_V0;
-            const bool first = g == 0, last = g == G - 1;
-            ok = wait(ms->full[bv], u >> 1) && wait(ms->full[B_DO], u);
-            if (ok && L < kC) ok = wait(ms->clean, dirty++);
-            if (!ok) break;
-            mma_kk(R, tile(B_DO), tile(bv), false);
-            mma_commit(&ms->mma_done);
-            ok = epi() && wait(ms->full[B_K], n) && wait(ms->full[B_S], u) && wait(ms->full[B_Q], n);
-            if (!ok) break;
-            mma_tm(dq, A0, tile(B_K), !first);
-            mma_tm(dq, A1, tile(B_S), true);
-            mma_commit(&ms->empty[B_S]);
-            mma_kk(R, tile(B_K), tile(B_Q), false);
-            mma_commit(&ms->mma_done);
-            ok = epi() && wait(ms->full[B_G], u);
-            if (!ok) break;
-            if (last) mbar_arrive(&ms->empty[B_K]);  // read by these MMAs and this epilogue step
-            mma_tm(R, A0, tile(B_DO), false);
-            mma_tk(R, A1, tile(B_G), true);
-            mma_commit(&ms->mma_done);
-            if (!(ok = epi())) break;
-            mma_kk(R, tile(bv), tile(B_DO), false);
+            const bool last = g == G - 1;
+            if (!(ok = wait(ms->full[B_K], n) && wait(ms->full[B_Q], n))) break;
+            if (L < kC && !(ok = wait(ms->clean, dirty++))) break;
+            mma_kk(T0, tile(B_K), tile(B_Q));
+            mma_commit(&ms->mma_done[0]);
+            if (!(ok = wait(ms->full[B_G], u))) break;
+            mma_kk(T1, tile(B_K), tile(B_G));
+            mma_commit(&ms->mma_done[1]);
+            if (!(ok = wait(ms->full[B_DO], u) && epi(0) && epi(1))) break;  // P^T; scaled T1
+            mma_tm(T1, T0, tile(B_DO), true);
+            mma_commit(&ms->mma_done[2]);
+            if (!(ok = wait(ms->full[B_V], u) && wait(ms->full[B_S], u) && epi(2))) break;  // dv out
+            mma_kk(T0, tile(B_DO), tile(B_V));
+            mma_commit(&ms->mma_done[3]);
+            mma_km(T1, tile(B_DO), tile(B_S));
             mma_commit(&ms->empty[B_DO]);
-            mma_commit(&ms->empty[bv]);
-            mma_commit(&ms->mma_done);
-            if (!(ok = epi())) break;
-            mma_tm(dk, A0, tile(B_Q), !first);
-            mma_tm(dk, A1, tile(B_G), true);
+            mma_commit(&ms->empty[B_S]);
+            mma_commit(&ms->mma_done[4]);
+            if (!(ok = epi(3))) break;  // P'
+            mma_km(T0, tile(B_V), tile(B_G));
             mma_commit(&ms->empty[B_G]);
+            mma_commit(&ms->empty[B_V]);
+            mma_commit(&ms->mma_done[5]);
+            if (!(ok = epi(4))) break;  // dq's first part
+            mma_km(dq, P, tile(B_K), true);
+            if (last) mma_commit(&ms->empty[B_K]);
+            if (!(ok = epi(5))) break;  // dk's first part
+            mma_mm(dk, P, tile(B_Q), true);
             if (last) mma_commit(&ms->empty[B_Q]);
         }
         if (!ok) break;
@@ -171,95 +174,115 @@ __device__ void multiply(const BackwardPass &p, uint32_t sbase, Misc *ms, uint32
     mbar_wait_bounded(&ms->drain, 0, kWaitLimit);
 }
 
+// The 128 threads that share a quarter of the lanes.
+__device__ __forceinline__ void quad_barrier(int quad) {
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + quad) : "memory");
+}
+
+// Whether any of the epilogue's threads has given up, the same answer for all.
+__device__ __forceinline__ bool any_gave_up(bool ok) {
+    uint32_t any;
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q;\n"
+        "setp.eq.u32 p, %1, 0;\n"
+        "barrier.cta.red.or.pred q, 5, %2, p;\n"
+        "selp.u32 %0, 1, 0, q;\n"
+        "}\n"
+        : "=r"(any)
+        : "r"((uint32_t)ok), "n"(kEpiThreads)
+        : "memory");
+    return any != 0;
+}
+
 __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t tmem, int G) {
     volatile int32_t *abort = &ms->abort;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
-    const int row = quad * 32 + lane;  // token of the chunk; columns 64 half ..
-    const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
-    float *up = ms->up[warp];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, cg = warp >> 2;
+    const int row = quad * 32 + lane;  // token of the chunk; columns 32 cg ..
+    const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16), tcol = trow + 32 * cg;
+    const float *up = nullptr;
     auto wait = [&](uint64_t &bar, uint32_t parity) { return role_wait(&bar, parity & 1, abort, p.err); };
-    uint32_t steps = 0;  // MMA steps waited for
-    auto mma = [&]() {
-        const bool ok = wait(ms->mma_done, steps);
-        ++steps;
+    // After a wait given up the remaining ones fail at once (abort is up), and a
+    // thread goes on through its barriers: they stay whole.
+    bool ok = true;
+    uint32_t u = 0;  // v-heads so far
+    auto product = [&](int k) {
+        ok = ok && wait(ms->mma_done[k], u);
         tc_fence_after_sync();
-        return ok;
     };
-    auto done = [&]() {
+    auto done = [&](int k) {
         tmem_wait_st();
         tc_fence_before_sync();
-        warp_arrive(&ms->epi_done);
+        warp_arrive(&ms->epi_done[k]);
     };
-    // A0 = R times scale lam^|row - column| where the column is not after
-    // (kLower) or not before the row, 0 elsewhere
-    auto mask = [&](bool lower, float l2) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int cb = 2 * half + b;  // columns 32 cb ..
-            uint32_t out[16];
-            if (lower ? cb > quad : cb < quad) {
-#pragma unroll
-                for (int x = 0; x < 16; ++x) out[x] = 0u;
-            } else {
-                float v[32];
-                tmem_ld32(trow + TM_R + 32 * cb, v);
-                tmem_wait_ld();
-                if (cb != quad) {
-                    const float f = p.scale * exp2f(l2 * (float)(lower ? row - 32 * cb - 31 : 32 * cb - row));
-#pragma unroll
-                    for (int x = 0; x < 32; x += 4) {  // lower: lam^{31-x}, read backwards
-                        const float4 w = *reinterpret_cast<const float4 *>(up + (lower ? 28 - x : x));
-                        v[x] *= f * (lower ? w.w : w.x);
-                        v[x + 1] *= f * (lower ? w.z : w.y);
-                        v[x + 2] *= f * (lower ? w.y : w.z);
-                        v[x + 3] *= f * (lower ? w.x : w.w);
-                    }
-                } else if (lower) {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        v[x] = x <= lane ? v[x] * (p.scale * up[(lane - x) & 31]) : 0.f;
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        v[x] = x >= lane ? v[x] * (p.scale * up[(x - lane) & 31]) : 0.f;
-                }
-#pragma unroll
-                for (int x = 0; x < 16; ++x) out[x] = pack_bf16(v[2 * x], v[2 * x + 1]);
-            }
-            tmem_st16u(trow + TM_A0 + 16 * cb, out);
-        }
-    };
-    // A1 = this thread's half row of a tile, times f
-    auto scaled = [&](int buf, float f) {
-        const uint8_t *t = sm + buf * kTile + half * kSub;
-        uint32_t out[32];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(t + sw128(row, 16 * c));
-            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&in[q]));
-                out[4 * c + q] = pack_bf16(a.x * f, a.y * f);
-            }
-        }
-        tmem_st32u(trow + TM_A1 + 32 * half, out);
-    };
-    // this thread's half row of an accumulator to its token's row of dst
-    auto write = [&](uint32_t col, void *dst, int64_t t0, int L, int H, int h, bool release) {
-        float v[64];
-        tmem_ld32(trow + col + 64 * half, *reinterpret_cast<float(*)[32]>(v));
-        tmem_ld32(trow + col + 64 * half + 32, *reinterpret_cast<float(*)[32]>(v + 32));
+    // this thread's 32 values of T0, times scale lam^|row - column| where the column is not
+    // after (kLower) or not before the row, 0 elsewhere, as 16 words of bf16 pairs
+    auto masked = [&](bool lower, float l2, uint32_t (&out)[16]) {
+        float v[32];
+        tmem_ld32(tcol + TM_T0, v);
         tmem_wait_ld();
-        if (release) done();
-        if (row >= L) return;
-        __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(dst) + ((t0 + row) * H + h) * (int64_t)kD + 64 * half;
+        if (lower ? cg > quad : cg < quad) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 16) {
+            for (int x = 0; x < 16; ++x) out[x] = 0u;
+        } else if (cg != quad) {
+            const float f = p.scale * exp2f(l2 * (float)(lower ? row - 32 * cg - 31 : 32 * cg - row));
+            const float2 f2 = make_float2(f, f);
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {  // lower: lam^{31-x}, read backwards
+                const float4 w = *reinterpret_cast<const float4 *>(up + (lower ? 28 - x : x));
+                const float2 w0 = lower ? make_float2(w.w, w.z) : make_float2(w.x, w.y);
+                const float2 w1 = lower ? make_float2(w.y, w.x) : make_float2(w.z, w.w);
+                out[x / 2] = pack_bf16(fmul2(make_float2(v[x], v[x + 1]), fmul2(w0, f2)));
+                out[x / 2 + 1] = pack_bf16(fmul2(make_float2(v[x + 2], v[x + 3]), fmul2(w1, f2)));
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+                const int d = lower ? lane - x : x - lane;
+                v[x] = d >= 0 ? v[x] * (p.scale * up[d & 31]) : 0.f;
+            }
+#pragma unroll
+            for (int x = 0; x < 16; ++x) out[x] = pack_bf16(v[2 * x], v[2 * x + 1]);
+        }
+    };
+    // this thread's 32 columns of an accumulator to its token's row of dst; product `release`
+    // (>= 0) is done with once they are read
+    auto write = [&](uint32_t col, void *dst, int64_t t0, int L, int H, int h, int release) {
+        float v[32];
+        tmem_ld32(tcol + col, v);
+        tmem_wait_ld();
+        if (release >= 0) done(release);
+        if (row >= L || !ok) return;
+        __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(dst) + ((t0 + row) * H + h) * (int64_t)kD + 32 * cg;
+#pragma unroll
+        for (int c = 0; c < 32; c += 16) {
             uint32_t w[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x) w[x] = pack_bf16(v[c + 2 * x], v[c + 2 * x + 1]);
             store_b256(d + c, w);
+        }
+    };
+    // acc = (first ? 0 : acc) + f T
+    auto add = [&](uint32_t acc, uint32_t T, float f, bool first) {
+        const float2 f2 = make_float2(f, f);
+#pragma unroll
+        for (int c = 0; c < 32; c += 16) {
+            float t[16], a[16];
+            tmem_ld16(tcol + T + c, t);
+            if (first) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) a[x] = 0.f;
+            } else {
+                tmem_ld16(tcol + acc + c, a);
+            }
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 16; x += 2) {
+                const float2 s = ffma2(f2, make_float2(t[x], t[x + 1]), make_float2(a[x], a[x + 1]));
+                a[x] = s.x;
+                a[x + 1] = s.y;
+            }
+            tmem_st16(tcol + acc + c, a);
         }
     };
     // rows past a partial chunk's end: 0 times a neighbour's NaN would reach every sum over tokens
@@ -271,62 +294,73 @@ __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t 
         }
     };
 
-    uint32_t u = 0;
     Item prev{0, -1, 0};
     for (uint32_t n = 0;; ++n) {
-        if (!wait(ms->item_full[n & 1], n >> 1)) return;
+        ok = ok && wait(ms->item_full[n & 1], n >> 1);
+        if (any_gave_up(ok)) return;
         const Item im = ms->item[n & 1];
         if (im.L < 0) break;
         warp_arrive(&ms->item_empty[n & 1]);
         for (int g = 0; g < G; ++g, ++u) {
-            const int h = im.j * G + g, bv = u & 1 ? B_V1 : B_V0;
+            const int h = im.j * G + g;
             const float l2 = p.log_decay[h] * kLog2e;
             if (im.L < kC) {
-                if (!wait(ms->full[bv], u >> 1) || !wait(ms->full[B_DO], u)) return;
-                if (g == 0 && (!wait(ms->full[B_K], n) || !wait(ms->full[B_Q], n))) return;
-                clear(bv, im.L);
-                clear(B_DO, im.L);
-                if (g == 0) {
-                    clear(B_K, im.L);
-                    clear(B_Q, im.L);
+                ok = ok && wait(ms->full[B_V], u) && wait(ms->full[B_DO], u) && wait(ms->full[B_K], n) &&
+                     wait(ms->full[B_Q], n);
+                if (ok) {
+                    clear(B_V, im.L);
+                    clear(B_DO, im.L);
+                    if (g == 0) {
+                        clear(B_K, im.L);
+                        clear(B_Q, im.L);
+                    }
+                    fence_proxy_async_smem();
                 }
-                fence_proxy_async_smem();
                 warp_arrive(&ms->clean);
             }
-            __syncwarp();
-            up[lane] = exp2f(l2 * (float)lane);
-            __syncwarp();
+            float *table = ms->up[u & 1][quad];
+            if (cg == 0) table[lane] = exp2f(l2 * (float)lane);
+            up = table;
+            quad_barrier(quad);
             const float fi = p.scale * exp2f(l2 * (float)(row + 1));
             const float fj = row < im.L ? exp2f(l2 * (float)(im.L - 1 - row)) : 0.f;
+            uint32_t out[16];
 
-            if (!mma()) return;  // R = dO V^T, and all of the previous item
+            product(0);  // T0 = K Q^T, and all of the previous item
             if (g == 0 && prev.L >= 0) {
-                write(TM_DQ, p.dq, prev.t0, prev.L, p.Hqk, prev.j, false);
-                write(TM_DK, p.dk, prev.t0, prev.L, p.Hqk, prev.j, false);
+                write(TM_DQ, p.dq, prev.t0, prev.L, p.Hqk, prev.j, -1);
+                write(TM_DK, p.dk, prev.t0, prev.L, p.Hqk, prev.j, -1);
             }
-            mask(true, l2);
-            if (!wait(ms->full[B_DO], u)) return;
-            scaled(B_DO, fi);
-            done();
-            if (!mma()) return;  // R = K Q^T
-            mask(false, l2);
-            if (!wait(ms->full[B_K], n)) return;
-            scaled(B_K, fj);
-            done();
-            if (!mma()) return;  // R = dv
-            if (!wait(ms->full[bv], u >> 1)) return;
-            scaled(bv, fj);
-            write(TM_R, p.dv, im.t0, im.L, p.Hv, h, true);
-            if (!mma()) return;  // R = V dO^T
-            mask(false, l2);
-            done();
+            masked(false, l2, out);
+            quad_barrier(quad);  // T0's rows have been read: P^T takes their place
+            tmem_st16u(trow + TM_T0 + 16 * cg, out);
+            done(0);
+            product(1);  // T1 = K G^T
+            add(TM_T1, TM_T1, fj, true);
+            done(1);
+            product(2);  // T1 = dv
+            write(TM_T1, p.dv, im.t0, im.L, p.Hv, h, 2);
+            product(3);  // T0 = dO V^T
+            masked(true, l2, out);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint4 *>(sm + OFF_P + (cg >> 1) * kSub + sw128(row, 64 * (cg & 1) + 16 * x)) =
+                    make_uint4(out[4 * x], out[4 * x + 1], out[4 * x + 2], out[4 * x + 3]);
+            fence_proxy_async_smem();
+            done(3);
+            product(4);  // T1 = dO S
+            add(TM_DQ, TM_T1, fi, g == 0);
+            done(4);
+            product(5);  // T0 = V G
+            add(TM_DK, TM_T0, fj, g == 0);
+            done(5);
         }
         prev = im;
     }
     if (prev.L >= 0) {
-        if (!mma()) return;
-        write(TM_DQ, p.dq, prev.t0, prev.L, p.Hqk, prev.j, false);
-        write(TM_DK, p.dk, prev.t0, prev.L, p.Hqk, prev.j, false);
+        product(0);
+        write(TM_DQ, p.dq, prev.t0, prev.L, p.Hqk, prev.j, -1);
+        write(TM_DK, p.dk, prev.t0, prev.L, p.Hqk, prev.j, -1);
     }
 }
 
@@ -346,8 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ms->item_full[b], 1);
             mbar_init(&ms->item_empty[b], 1 + kEpiWarps);
         }
-        mbar_init(&ms->mma_done, 1);
-        mbar_init(&ms->epi_done, kEpiWarps);
+        for (int b = 0; b < kSteps; ++b) {
+            mbar_init(&ms->mma_done[b], 1);
+            mbar_init(&ms->epi_done[b], kEpiWarps);
+        }
         mbar_init(&ms->clean, kEpiWarps);
         mbar_init(&ms->drain, 1);
         ms->abort = 0;

@@ -45,21 +45,26 @@ __device__ __forceinline__ uint64_t step_k(uint64_t d, int ks) {
 __device__ __forceinline__ uint64_t step_m(uint64_t d, int ks) { return d + (uint64_t)(ks * 2048 >> 4); }
 
 // D (+)= A B over 128 summed elements, operands in shared memory; letters as above.
-__device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t b, bool acc) {
+__device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t b, bool acc = false) {
     const uint64_t da = desc_k(a), db = desc_k(b);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) mma_f16_ss(d, step_k(da, ks), step_k(db, ks), IDESC_KK, acc || ks);
 }
-// A from tensor memory (K-major, 64 columns of packed pairs), B MN-major or K-major.
-__device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a_tmem, uint32_t b, bool acc) {
+__device__ __forceinline__ void mma_km(uint32_t d, uint32_t a, uint32_t b, bool acc = false) {
+    const uint64_t da = desc_k(a), db = desc_m(b);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) mma_f16_ss(d, step_k(da, ks), step_m(db, ks), IDESC_KM, acc || ks);
+}
+__device__ __forceinline__ void mma_mm(uint32_t d, uint32_t a, uint32_t b, bool acc = false) {
+    const uint64_t da = desc_m(a), db = desc_m(b);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) mma_f16_ss(d, step_m(da, ks), step_m(db, ks), IDESC_MM, acc || ks);
+}
+// A from tensor memory (K-major, 64 columns of packed pairs), B MN-major.
+__device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a_tmem, uint32_t b, bool acc = false) {
     const uint64_t db = desc_m(b);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) mma_f16_ts(d, a_tmem + 8 * ks, step_m(db, ks), IDESC_KM, acc || ks);
-}
-__device__ __forceinline__ void mma_tk(uint32_t d, uint32_t a_tmem, uint32_t b, bool acc) {
-    const uint64_t db = desc_k(b);
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) mma_f16_ts(d, a_tmem + 8 * ks, step_k(db, ks), IDESC_KK, acc || ks);
 }
 
 // 32 bytes in one store: a whole memory sector per thread.
