@@ -3,8 +3,13 @@
 //
 // Bound by HBM bandwidth on the state, 8 Dv Dk bytes read and written per unit;
 // each row is loaded, updated, reduced against q and stored by the same lanes.
-// Row i of Dk fp32 values is spread over Dk / 4 lanes as float4.  A CTA of 8
-// warps serves one unit, every warp with kRows row groups in flight.
+// Row i of Dk fp32 values is spread over Dk / 4 lanes as float4.
+//
+// Dk = 128, the workload's: a warp takes kRows rows of a unit at once, all their
+// loads in flight, and sums their dot products together by recursive halving
+// (kRows shuffles and one, instead of 5 kRows).  16 rows a warp when there are
+// units enough to fill the GPU so, 4 when there are few (latency).
+// Other Dk: a CTA of 8 warps serves one unit, with kRows row groups in flight.
 #include "linear.cuh"
 
 namespace gdn {
@@ -73,6 +78,70 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_linear_decode_kernel(DecodeSt
     }
 }
 
+// Sums each of R values over the warp: lane L returns the sum of value L / (32 / R).
+template <int R>
+__device__ __forceinline__ float transposed_sum(float (&v)[R], int lane) {
+#pragma unroll
+    for (int n = R, off = 16; n > 1; n /= 2, off /= 2) {
+        const bool up = lane & off;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float send = up ? v[i] : v[i + n / 2], keep = up ? v[i + n / 2] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+        }
+    }
+#pragma unroll
+    for (int off = 16 / R; off > 0; off /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+    return v[0];
+}
+
+template <int R>
+__global__ void __launch_bounds__(kWarps * 32) gdn_linear_decode128_kernel(DecodeStep d, int blocks) {
+    const int unit = blockIdx.x / blocks, h = unit % d.Hv, n = unit / d.Hv, j = h / (d.Hv / d.Hqk);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int i0 = ((blockIdx.x % blocks) * kWarps + warp) * R;  // this warp's rows
+    const int64_t slot = state_index(d.map, n);
+    if (slot < 0) {  // a bad slot index: this unit writes nothing
+        if (threadIdx.x == 0) raise_error(d.err, GDN_ERR_BAD_SLOT);
+        return;
+    }
+    if (i0 >= d.Dv) return;
+    const bool fresh = state_fresh(d.map, n);
+    float4 *st = reinterpret_cast<float4 *>(d.state + ((slot * d.Hv + h) * (int64_t)d.Dv + i0) * 128) + lane;
+    const int rows = d.Dv - i0;  // those of them that exist (R or more: all)
+    float4 s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        s[r] = !fresh && r < rows ? __ldcs(st + 32 * r) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const int64_t qk = ((int64_t)n * d.Hqk + j) * 128 + 4 * lane, vo = (int64_t)unit * d.Dv + i0;
+    const float4 kk = load4(d.k, qk, d.dtype), qq = load4(d.q, qk, d.dtype);
+    const float vl = lane < R && lane < rows ? load_io(d.v, vo + lane, d.dtype) : 0.f;
+    const Decay decay(d.log_decay[h]);
+    auto times = [&](float x) { return decay.slow ? decay.times<true>(x) : decay.times<false>(x); };
+    float dot[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float v = __shfl_sync(0xffffffffu, vl, r);
+        s[r].x = fmaf(v, kk.x, times(s[r].x));
+        s[r].y = fmaf(v, kk.y, times(s[r].y));
+        s[r].z = fmaf(v, kk.z, times(s[r].z));
+        s[r].w = fmaf(v, kk.w, times(s[r].w));
+        if (r < rows) __stcs(st + 32 * r, s[r]);
+        dot[r] = s[r].x * qq.x + s[r].y * qq.y + s[r].z * qq.z + s[r].w * qq.w;
+    }
+    const float o = transposed_sum<R>(dot, lane);
+    const int r = lane / (32 / R);
+    if (lane % (32 / R) == 0 && r < rows) store_io(d.o, vo + r, o * d.scale, d.dtype);
+}
+
+template <int R>
+cudaError_t launch128(const DecodeStep &d, int64_t units, cudaStream_t s) {
+    const int blocks = (d.Dv + kWarps * R - 1) / (kWarps * R);
+    if (units * blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    gdn_linear_decode128_kernel<R><<<(unsigned)(units * blocks), kWarps * 32, 0, s>>>(d, blocks);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_decode(const DecodeStep &d, cudaStream_t s) {
@@ -84,7 +153,7 @@ cudaError_t launch_decode(const DecodeStep &d, cudaStream_t s) {
         case 16: gdn_linear_decode_kernel<16><<<grid, block, 0, s>>>(d); break;
         case 32: gdn_linear_decode_kernel<32><<<grid, block, 0, s>>>(d); break;
         case 64: gdn_linear_decode_kernel<64><<<grid, block, 0, s>>>(d); break;
-        case 128: gdn_linear_decode_kernel<128><<<grid, block, 0, s>>>(d); break;
+        case 128: return units * ((d.Dv + 127) / 128) >= 296 ? launch128<16>(d, units, s) : launch128<4>(d, units, s);
         default: return cudaErrorInvalidValue;
     }
     return cudaGetLastError();

@@ -116,63 +116,100 @@ __device__ __forceinline__ void angles(const RopeArgs &a, int64_t t0, int n, flo
     }
 }
 
+__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
 // Turns the lane's 8 elements (block l of the row) by its token's angles;
 // sign = -1 turns them back.
 template <int LPR>
 __device__ __forceinline__ void rotate(float (&y)[8], int l, const float *c, const float *s, int rot,
                                        int interleaved, float sign) {
     const int hb = rot / 16;  // blocks per half of the rotated dimensions
+    const bool in = l < 2 * hb;
     if (interleaved) {
-        if (l < 2 * hb) {
+        if (in) {
+            const float4 c4 = *reinterpret_cast<const float4 *>(c + 4 * l);
+            const float4 s4 = *reinterpret_cast<const float4 *>(s + 4 * l);
+            const float cv[4] = {c4.x, c4.y, c4.z, c4.w}, sv[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float cc = c[4 * l + j], ss = sign * s[4 * l + j], p = y[2 * j], q = y[2 * j + 1];
-                y[2 * j] = p * cc - q * ss;
-                y[2 * j + 1] = q * cc + p * ss;
+                const float ss = sign * sv[j], p = y[2 * j], q = y[2 * j + 1];
+                y[2 * j] = p * cv[j] - q * ss;
+                y[2 * j + 1] = q * cv[j] + p * ss;
             }
         }
         return;
     }
-    const bool in = l < 2 * hb, lower = l < hb;
+    if (hb == 0) return;
+    const bool lower = l < hb;
     const int lane = threadIdx.x & 31, src = in ? (lower ? lane + hb : lane - hb) : lane;
-    const int b = lower ? l : l - hb;
+    const int b = in ? (lower ? l : l - hb) : 0;
     const float sg = lower ? -sign : sign;
+    float cv[8], sv[8];
+    load8(c + 8 * b, cv);
+    load8(s + 8 * b, sv);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float other = __shfl_sync(0xffffffffu, y[j], src);
-        if (in) y[j] = y[j] * c[8 * b + j] + sg * other * s[8 * b + j];
+        if (in) y[j] = y[j] * cv[j] + sg * other * sv[j];
     }
 }
 
+// A CTA's rows: `first` and the following ones, as tokens and heads.  The one
+// 64-bit division is the CTA's; a row's place is 32-bit arithmetic from there.
+struct Rows {
+    int64_t t0;     // token of the first row
+    uint32_t h0;    // its head
+    uint32_t n;     // rows
+    uint32_t n_tok;
+    __device__ __forceinline__ Rows(const RopeArgs &a, int64_t first, int per) {
+        t0 = first / a.H;
+        h0 = (uint32_t)(first - t0 * a.H);
+        n = (uint32_t)(a.rows - first < per ? a.rows - first : per);
+        n_tok = (h0 + n - 1) / (uint32_t)a.H + 1;
+    }
+};
+// Row r of them: its token (from t0), whether it is a key's, its elements' offset within the token.
+template <int D>
+struct Row {
+    uint32_t tok;
+    int z, off;
+    __device__ __forceinline__ Row(const RopeArgs &a, const Rows &rows, uint32_t r, int l) {
+        const uint32_t x = rows.h0 + r;
+        tok = x / (uint32_t)a.H;
+        const int h = (int)(x - tok * (uint32_t)a.H);
+        z = h >= a.Hq;
+        off = (h - (z ? a.Hq : 0)) * D + 8 * l;
+    }
+};
+
 template <class E, int D, int kIter>
 __global__ void __launch_bounds__(kThreads) gdn_qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
-    extern __shared__ float smem[];
+    extern __shared__ __align__(16) float smem[];
     constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
     const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
-    const int64_t first = (int64_t)blockIdx.x * (GROUPS * kIter);
-    const int64_t t_first = first / a.H;
-    const int64_t last = first + GROUPS * kIter < a.rows ? first + GROUPS * kIter : a.rows;
-    const int n_tok = (int)((last - 1) / a.H - t_first) + 1;
+    const Rows rows(a, (int64_t)blockIdx.x * (GROUPS * kIter), GROUPS * kIter);
     Vec8<E> x[kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-        const int64_t row = first + i * GROUPS + grp;
-        if (row < a.rows) {
-            const int64_t t = row / a.H;
-            const int h = (int)(row - t * a.H), z = h >= a.Hq;
-            x[i].load(a.x[z], t * a.x_stride[z] + (int64_t)(h - (z ? a.Hq : 0)) * D + 8 * l);
+        const uint32_t r = i * GROUPS + grp;
+        if (r < rows.n) {
+            const Row<D> w(a, rows, r, l);
+            x[i].load(a.x[w.z], (rows.t0 + w.tok) * a.x_stride[w.z] + w.off);
         }
     }
     const int half = a.rot / 2;
-    float *cosines = smem, *sines = smem + n_tok * half;
-    angles(a, t_first, n_tok, cosines, sines);
+    float *cosines = smem, *sines = smem + rows.n_tok * half;
+    angles(a, rows.t0, (int)rows.n_tok, cosines, sines);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-        const int64_t row = first + i * GROUPS + grp;
-        const bool live = row < a.rows;  // every lane runs the shuffles
-        const int64_t t = live ? row / a.H : t_first;
-        const int h = live ? (int)(row - t * a.H) : 0, z = h >= a.Hq;
+        const uint32_t r = i * GROUPS + grp;
+        const bool live = r < rows.n;  // every lane runs the shuffles
+        const Row<D> w(a, rows, live ? r : 0, l);
         float y[8];
         if (live) {
             x[i].get(y);
@@ -183,22 +220,20 @@ __global__ void __launch_bounds__(kThreads) gdn_qk_norm_rope_kernel(const __grid
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
-        const float r = rsqrtf(group_sum<LPR>(ss) * (1.f / D) + a.eps);
-        const float *w = a.w[z];
-        if (w) {
-            const float4 w0 = *reinterpret_cast<const float4 *>(w + 8 * l);
-            const float4 w1 = *reinterpret_cast<const float4 *>(w + 8 * l + 4);
-            const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        const float rms = rsqrtf(group_sum<LPR>(ss) * (1.f / D) + a.eps);
+        const float *wt = a.w[w.z];
+        if (wt) {
+            float wv[8];
+            load8(wt + 8 * l, wv);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= r * wv[j];
+            for (int j = 0; j < 8; ++j) y[j] *= rms * wv[j];
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= r;
+            for (int j = 0; j < 8; ++j) y[j] *= rms;
         }
-        const int off = (int)(t - t_first) * half;
+        const int off = (int)w.tok * half;
         rotate<LPR>(y, l, cosines + off, sines + off, a.rot, a.interleaved, 1.f);
-        if (live)
-            Vec8<E>::store(a.out[z], t * a.out_stride[z] + (int64_t)(h - (z ? a.Hq : 0)) * D + 8 * l, y);
+        if (live) Vec8<E>::store(a.out[w.z], (rows.t0 + w.tok) * a.out_stride[w.z] + w.off, y);
     }
 }
 
@@ -208,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) gdn_qk_norm_rope_kernel(const __grid
 template <class E, int D, int kIter>
 __global__ void __launch_bounds__(kThreads)
     gdn_qk_norm_rope_backward_kernel(const __grid_constant__ RopeArgs a) {
-    extern __shared__ float smem[];
+    extern __shared__ __align__(16) float smem[];
     constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
     const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
     const int half = a.rot / 2;
@@ -219,31 +254,26 @@ __global__ void __launch_bounds__(kThreads)
         for (int j = 0; j < 8; ++j) acc[z][j] = 0.f;
     for (int64_t first = (int64_t)blockIdx.x * (GROUPS * kIter); first < a.rows;
          first += (int64_t)gridDim.x * (GROUPS * kIter)) {
-        const int64_t t_first = first / a.H;
-        const int64_t last = first + GROUPS * kIter < a.rows ? first + GROUPS * kIter : a.rows;
-        const int n_tok = (int)((last - 1) / a.H - t_first) + 1;
+        const Rows rows(a, first, GROUPS * kIter);
         Vec8<E> x[kIter], g[kIter];
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
-            const int64_t row = first + i * GROUPS + grp;
-            if (row < a.rows) {
-                const int64_t t = row / a.H;
-                const int h = (int)(row - t * a.H), z = h >= a.Hq;
-                const int64_t e = (int64_t)(h - (z ? a.Hq : 0)) * D + 8 * l;
-                x[i].load(a.x[z], t * a.x_stride[z] + e);
-                g[i].load(a.dz[z], t * a.dz_stride[z] + e);
+            const uint32_t r = i * GROUPS + grp;
+            if (r < rows.n) {
+                const Row<D> w(a, rows, r, l);
+                x[i].load(a.x[w.z], (rows.t0 + w.tok) * a.x_stride[w.z] + w.off);
+                g[i].load(a.dz[w.z], (rows.t0 + w.tok) * a.dz_stride[w.z] + w.off);
             }
         }
         __syncthreads();  // the previous block's angles have been read
-        float *cosines = smem, *sines = smem + n_tok * half;
-        angles(a, t_first, n_tok, cosines, sines);
+        float *cosines = smem, *sines = smem + rows.n_tok * half;
+        angles(a, rows.t0, (int)rows.n_tok, cosines, sines);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
-            const int64_t row = first + i * GROUPS + grp;
-            const bool live = row < a.rows;
-            const int64_t t = live ? row / a.H : t_first;
-            const int h = live ? (int)(row - t * a.H) : 0, z = h >= a.Hq;
+            const uint32_t r = i * GROUPS + grp;
+            const bool live = r < rows.n;
+            const Row<D> w(a, rows, live ? r : 0, l);
             float n[8], dy[8];
             if (live) {
                 x[i].get(n);
@@ -255,27 +285,30 @@ __global__ void __launch_bounds__(kThreads)
             float ss = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) ss = fmaf(n[j], n[j], ss);
-            const float r = rsqrtf(group_sum<LPR>(ss) * (1.f / D) + a.eps);
-            const int off = (int)(t - t_first) * half;
+            const float rms = rsqrtf(group_sum<LPR>(ss) * (1.f / D) + a.eps);
+            const int off = (int)w.tok * half;
             rotate<LPR>(dy, l, cosines + off, sines + off, a.rot, a.interleaved, -1.f);
-            const float *w = a.w[z];
+            float wv[8];
+            if (a.w[w.z]) {
+                load8(a.w[w.z] + 8 * l, wv);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) wv[j] = 1.f;
+            }
             float dot = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                n[j] *= r;
-                const float dn = dy[j] * n[j];
-                if (live) {
-                    if (z) acc[1][j] += dn;
-                    else acc[0][j] += dn;
-                }
-                dy[j] *= w ? w[8 * l + j] : 1.f;
+                n[j] *= rms;
+                const float dn = dy[j] * n[j];  // a dead row's is 0 times 0
+                acc[0][j] += w.z ? 0.f : dn;
+                acc[1][j] += w.z ? dn : 0.f;
+                dy[j] *= wv[j];
                 dot = fmaf(dy[j], n[j], dot);
             }
             dot = group_sum<LPR>(dot) * (1.f / D);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dy[j] = r * (dy[j] - n[j] * dot);
-            if (live)
-                Vec8<E>::store(a.out[z], t * a.out_stride[z] + (int64_t)(h - (z ? a.Hq : 0)) * D + 8 * l, dy);
+            for (int j = 0; j < 8; ++j) dy[j] = rms * (dy[j] - n[j] * dot);
+            if (live) Vec8<E>::store(a.out[w.z], (rows.t0 + w.tok) * a.out_stride[w.z] + w.off, dy);
         }
     }
     if (!a.dw_part) return;
@@ -333,12 +366,12 @@ cudaError_t launch_forward(const RopeArgs &a, cudaStream_t s) {
 
 template <class E, int D>
 cudaError_t launch_backward(const RopeArgs &a, float *dwq, float *dwk, cudaStream_t s) {
-    constexpr int GROUPS = kThreads / (D / 8);
-    const int64_t blocks = (a.rows + GROUPS * 2 - 1) / (GROUPS * 2);
+    constexpr int GROUPS = kThreads / (D / 8), kIter = sizeof(E) == 2 ? 4 : 2;
+    const int64_t blocks = (a.rows + GROUPS * kIter - 1) / (GROUPS * kIter);
     const int ctas = (int)(blocks < kBackwardCtas ? blocks : kBackwardCtas);
-    size_t smem = (size_t)tokens_of(GROUPS * 2, a.H) * a.rot * sizeof(float);
+    size_t smem = (size_t)tokens_of(GROUPS * kIter, a.H) * a.rot * sizeof(float);
     if (smem < (size_t)GROUPS * D * sizeof(float)) smem = (size_t)GROUPS * D * sizeof(float);
-    auto *fn = gdn_qk_norm_rope_backward_kernel<E, D, 2>;
+    auto *fn = gdn_qk_norm_rope_backward_kernel<E, D, kIter>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
