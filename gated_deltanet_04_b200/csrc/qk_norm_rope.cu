@@ -15,12 +15,15 @@
 // on at most half a turn.  A CTA computes them once per token it covers and
 // keeps them in shared memory for all its heads.
 //
-// Bound by HBM bandwidth: x is read once, z written once (backward: x and dz
-// read, dx written).  A row is spread over D / 8 lanes with 8 elements each;
-// rotation partners are another lane's same elements (rot % 16 == 0), one
-// shuffle away.  A CTA takes kIter rows per lane group with all their loads in
-// flight before the angles are computed.
+// Bound by HBM bandwidth, x read once and z written once (backward: x and dz
+// read, dx written), and nearly by instruction issue: a row is spread over D / 8
+// lanes with two pieces of 4 elements each, chosen so that a lane holds both of
+// every pair it turns, and the arithmetic is on pairs of floats.  (With 8
+// consecutive elements per lane and partners exchanged by shuffles it took twice
+// the instructions and twice the time.)  A CTA takes kIter rows per lane group
+// with all their loads in flight before the angles are computed.
 #include "gdn_internal.cuh"
+#include "sm100.cuh"
 #include "trace.cuh"
 
 namespace gdn {
@@ -42,53 +45,74 @@ struct RopeArgs {
     int32_t last[kMaxAxes];    // frequency i belongs to the first axis with i < last[axis]
     float eps;
     int32_t Hq, H, rot, interleaved;
+    uint32_t inv_h, inv_half;  // ceil(2^32 / H) (H > 1), ceil(2^32 / (rot / 2))
+    int32_t blocks;            // blocks of kIter rows per lane group that share their angles
     int64_t T, rows;           // rows = T * H
 };
 
-// 8 consecutive elements of a row as fp32.
+using sm100::ffma2;
+using sm100::fmul2;
+
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+
+// Where a lane's 8 elements of a row are: 4 from p0, 4 from p1.  Rotated
+// halves: the same 4 of the lower and of the upper half; otherwise (interleaved
+// pairs, elements that are not rotated) 8 in a row.  `angle`: the lane's first
+// frequency, or -1.
+struct Pieces {
+    int p0, p1, angle;
+    __device__ __forceinline__ Pieces(int l, int rot, int interleaved) {
+        const bool in = 8 * l < rot;
+        p0 = in && !interleaved ? 4 * l : 8 * l;
+        p1 = in && !interleaved ? rot / 2 + 4 * l : 8 * l + 4;
+        angle = in ? 4 * l : -1;
+    }
+};
+
+// A lane's two pieces of a row, as loaded, and as four pairs of floats.
 template <class E>
 struct Vec8;
 template <>
 struct Vec8<__nv_bfloat16> {
-    uint4 v;
-    __device__ __forceinline__ void load(const void *p, int64_t i) {
-        v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i);
+    uint2 a, b;
+    __device__ __forceinline__ void load(const void *p, int64_t i, const Pieces &c) {
+        a = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i + c.p0);
+        b = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i + c.p1);
     }
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 t = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[j]));
-            f[2 * j] = t.x;
-            f[2 * j + 1] = t.y;
-        }
+    static __device__ __forceinline__ float2 wide(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
-    static __device__ __forceinline__ void store(void *p, int64_t i, const float (&f)[8]) {
-        uint32_t u[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-            u[j] = *reinterpret_cast<const uint32_t *>(&t);
-        }
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + i) = make_uint4(u[0], u[1], u[2], u[3]);
+    __device__ __forceinline__ void get(float2 (&f)[4]) const {
+        f[0] = wide(a.x);
+        f[1] = wide(a.y);
+        f[2] = wide(b.x);
+        f[3] = wide(b.y);
+    }
+    static __device__ __forceinline__ uint32_t narrow(float2 x) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(x.x, x.y);
+        return *reinterpret_cast<const uint32_t *>(&t);
+    }
+    static __device__ __forceinline__ void store(void *p, int64_t i, const Pieces &c, const float2 (&f)[4]) {
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p) + i + c.p0) = make_uint2(narrow(f[0]), narrow(f[1]));
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p) + i + c.p1) = make_uint2(narrow(f[2]), narrow(f[3]));
     }
 };
 template <>
 struct Vec8<float> {
     float4 a, b;
-    __device__ __forceinline__ void load(const void *p, int64_t i) {
-        const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-        a = s[0];
-        b = s[1];
+    __device__ __forceinline__ void load(const void *p, int64_t i, const Pieces &c) {
+        a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + c.p0);
+        b = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + c.p1);
     }
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    __device__ __forceinline__ void get(float2 (&f)[4]) const {
+        f[0] = make_float2(a.x, a.y);
+        f[1] = make_float2(a.z, a.w);
+        f[2] = make_float2(b.x, b.y);
+        f[3] = make_float2(b.z, b.w);
     }
-    static __device__ __forceinline__ void store(void *p, int64_t i, const float (&f)[8]) {
-        float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-        d[0] = make_float4(f[0], f[1], f[2], f[3]);
-        d[1] = make_float4(f[4], f[5], f[6], f[7]);
+    static __device__ __forceinline__ void store(void *p, int64_t i, const Pieces &c, const float2 (&f)[4]) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p) + i + c.p0) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+        *reinterpret_cast<float4 *>(static_cast<float *>(p) + i + c.p1) = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
     }
 };
 
@@ -99,16 +123,15 @@ __device__ __forceinline__ float group_sum(float x) {
     return x;
 }
 
-// cos and sin of tokens t0 .. t0 + n - 1 into cs[token][rot/2] (cosines, then sines).
-__device__ __forceinline__ void angles(const RopeArgs &a, int64_t t0, int n, float *cosines, float *sines) {
-    const int half = a.rot / 2;
-    for (int i = threadIdx.x; i < n * half; i += kThreads) {
-        const int64_t t = t0 + i / half;
-        const int f = i % half;
+// cos and sin of tokens t0 .. t0 + n - 1 into [token][rot/2] each.
+__device__ __forceinline__ void angles(const RopeArgs &a, int64_t t0, uint32_t n, float *cosines, float *sines) {
+    const uint32_t half = (uint32_t)a.rot / 2;
+    for (uint32_t i = threadIdx.x; i < n * half; i += kThreads) {
+        const uint32_t tok = __umulhi(i, a.inv_half), f = i - tok * half;  // i half < 2^32: exact
         int axis = 0;
-        while (axis < kMaxAxes - 1 && f >= a.last[axis]) ++axis;
+        while (axis < kMaxAxes - 1 && (int)f >= a.last[axis]) ++axis;
         // whole turns removed in fp64: |turns| < 2^31 leaves 2^-22 of a turn at worst
-        const double turns = (double)a.pos[axis * a.T + t] * ((double)a.inv_freq[f] * 0.15915494309189533577);
+        const double turns = (double)a.pos[axis * a.T + t0 + tok] * ((double)a.inv_freq[f] * 0.15915494309189533577);
         float s, c;
         sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
         cosines[i] = c;
@@ -116,199 +139,210 @@ __device__ __forceinline__ void angles(const RopeArgs &a, int64_t t0, int n, flo
     }
 }
 
-__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+// The lane's pieces of an fp32 row (weights).
+__device__ __forceinline__ void load_pieces(const float *p, const Pieces &c, float2 (&f)[4]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p + c.p0), b = *reinterpret_cast<const float4 *>(p + c.p1);
+    f[0] = make_float2(a.x, a.y);
+    f[1] = make_float2(a.z, a.w);
+    f[2] = make_float2(b.x, b.y);
+    f[3] = make_float2(b.z, b.w);
 }
 
-// Turns the lane's 8 elements (block l of the row) by its token's angles;
-// sign = -1 turns them back.
-template <int LPR>
-__device__ __forceinline__ void rotate(float (&y)[8], int l, const float *c, const float *s, int rot,
+// Turns the lane's pairs by its token's angles; sign = -1 turns them back.
+__device__ __forceinline__ void rotate(float2 (&y)[4], const Pieces &c, const float *cosines, const float *sines,
                                        int interleaved, float sign) {
-    const int hb = rot / 16;  // blocks per half of the rotated dimensions
-    const bool in = l < 2 * hb;
+    if (c.angle < 0) return;
+    const float4 c4 = *reinterpret_cast<const float4 *>(cosines + c.angle);
+    const float4 s4 = *reinterpret_cast<const float4 *>(sines + c.angle);
     if (interleaved) {
-        if (in) {
-            const float4 c4 = *reinterpret_cast<const float4 *>(c + 4 * l);
-            const float4 s4 = *reinterpret_cast<const float4 *>(s + 4 * l);
-            const float cv[4] = {c4.x, c4.y, c4.z, c4.w}, sv[4] = {s4.x, s4.y, s4.z, s4.w};
+        const float cv[4] = {c4.x, c4.y, c4.z, c4.w}, sv[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float ss = sign * sv[j], p = y[2 * j], q = y[2 * j + 1];
-                y[2 * j] = p * cv[j] - q * ss;
-                y[2 * j + 1] = q * cv[j] + p * ss;
-            }
+        for (int j = 0; j < 4; ++j) {
+            const float ss = sign * sv[j];
+            y[j] = make_float2(y[j].x * cv[j] - y[j].y * ss, y[j].y * cv[j] + y[j].x * ss);
         }
         return;
     }
-    if (hb == 0) return;
-    const bool lower = l < hb;
-    const int lane = threadIdx.x & 31, src = in ? (lower ? lane + hb : lane - hb) : lane;
-    const int b = in ? (lower ? l : l - hb) : 0;
-    const float sg = lower ? -sign : sign;
-    float cv[8], sv[8];
-    load8(c + 8 * b, cv);
-    load8(s + 8 * b, sv);
+    const float2 cc[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+    const float2 ss[2] = {fmul2(make_float2(s4.x, s4.y), splat(sign)), fmul2(make_float2(s4.z, s4.w), splat(sign))};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float other = __shfl_sync(0xffffffffu, y[j], src);
-        if (in) y[j] = y[j] * cv[j] + sg * other * sv[j];
+    for (int j = 0; j < 2; ++j) {
+        const float2 lo = y[j], hi = y[2 + j];
+        y[j] = ffma2(lo, cc[j], fmul2(hi, make_float2(-ss[j].x, -ss[j].y)));
+        y[2 + j] = ffma2(hi, cc[j], fmul2(lo, ss[j]));
     }
 }
 
-// A CTA's rows: `first` and the following ones, as tokens and heads.  The one
-// 64-bit division is the CTA's; a row's place is 32-bit arithmetic from there.
+__device__ __forceinline__ float dot8(const float2 (&a)[4], const float2 (&b)[4]) {
+    float2 s = fmul2(a[0], b[0]);
+#pragma unroll
+    for (int j = 1; j < 4; ++j) s = ffma2(a[j], b[j], s);
+    return s.x + s.y;
+}
+
+// A CTA's rows: `first` and the following ones, as tokens and heads.
 struct Rows {
     int64_t t0;     // token of the first row
     uint32_t h0;    // its head
     uint32_t n;     // rows
     uint32_t n_tok;
     __device__ __forceinline__ Rows(const RopeArgs &a, int64_t first, int per) {
-        t0 = first / a.H;
+        // (a 64-bit division only where 32 bits do not hold the row)
+        t0 = a.rows >> 32 ? first / a.H : (int64_t)((uint32_t)first / (uint32_t)a.H);
         h0 = (uint32_t)(first - t0 * a.H);
         n = (uint32_t)(a.rows - first < per ? a.rows - first : per);
         n_tok = (h0 + n - 1) / (uint32_t)a.H + 1;
     }
 };
-// Row r of them: its token (from t0), whether it is a key's, its elements' offset within the token.
+// Row r of them: its token (from t0), whether it is a key's, its offset within the token.
 template <int D>
 struct Row {
     uint32_t tok;
     int z, off;
-    __device__ __forceinline__ Row(const RopeArgs &a, const Rows &rows, uint32_t r, int l) {
-        const uint32_t x = rows.h0 + r;
-        tok = x / (uint32_t)a.H;
+    __device__ __forceinline__ Row(const RopeArgs &a, const Rows &rows, uint32_t r) {
+        const uint32_t x = rows.h0 + r;  // x H < 2^32: the product with ceil(2^32 / H) divides exactly
+        tok = a.H == 1 ? x : __umulhi(x, a.inv_h);
         const int h = (int)(x - tok * (uint32_t)a.H);
         z = h >= a.Hq;
-        off = (h - (z ? a.Hq : 0)) * D + 8 * l;
+        off = (h - (z ? a.Hq : 0)) * D;
     }
 };
 
+// A CTA's rows go in a.blocks blocks of kIter rows per lane group: the next
+// block's loads are in flight while one is computed, and the angles of all their
+// tokens are computed once, before the first.
 template <class E, int D, int kIter>
 __global__ void __launch_bounds__(kThreads) gdn_qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
     extern __shared__ __align__(16) float smem[];
-    constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
+    constexpr int LPR = D / 8, GROUPS = kThreads / LPR, kBlock = GROUPS * kIter;
     const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
-    const Rows rows(a, (int64_t)blockIdx.x * (GROUPS * kIter), GROUPS * kIter);
-    Vec8<E> x[kIter];
+    const Pieces c(l, a.rot, a.interleaved);
+    const Rows rows(a, (int64_t)blockIdx.x * (kBlock * a.blocks), kBlock * a.blocks);
+    Vec8<E> next[kIter];
+    auto load = [&](uint32_t r0) {
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-        const uint32_t r = i * GROUPS + grp;
-        if (r < rows.n) {
-            const Row<D> w(a, rows, r, l);
-            x[i].load(a.x[w.z], (rows.t0 + w.tok) * a.x_stride[w.z] + w.off);
+        for (int i = 0; i < kIter; ++i) {
+            const uint32_t r = r0 + i * GROUPS;
+            if (r < rows.n) {
+                const Row<D> w(a, rows, r);
+                next[i].load(a.x[w.z], (rows.t0 + w.tok) * a.x_stride[w.z] + w.off, c);
+            }
         }
-    }
+    };
+    load(grp);
     const int half = a.rot / 2;
     float *cosines = smem, *sines = smem + rows.n_tok * half;
-    angles(a, rows.t0, (int)rows.n_tok, cosines, sines);
+    angles(a, rows.t0, rows.n_tok, cosines, sines);
     __syncthreads();
+    for (uint32_t b0 = 0; b0 < rows.n; b0 += kBlock) {
+        Vec8<E> x[kIter];
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-        const uint32_t r = i * GROUPS + grp;
-        const bool live = r < rows.n;  // every lane runs the shuffles
-        const Row<D> w(a, rows, live ? r : 0, l);
-        float y[8];
-        if (live) {
+        for (int i = 0; i < kIter; ++i) x[i] = next[i];
+        load(b0 + kBlock + grp);
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+            const uint32_t r = b0 + i * GROUPS + grp;
+            const bool live = r < rows.n;  // every lane runs the shuffles
+            const Row<D> w(a, rows, live ? r : 0);
+            float2 y[4];
             x[i].get(y);
-        } else {
+            const float2 rms = splat(rsqrtf(group_sum<LPR>(dot8(y, y)) * (1.f / D) + a.eps));
+            if (a.w[w.z]) {
+                float2 wv[4];
+                load_pieces(a.w[w.z], c, wv);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = 0.f;
+                for (int j = 0; j < 4; ++j) y[j] = fmul2(y[j], fmul2(rms, wv[j]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = fmul2(y[j], rms);
+            }
+            const int off = (int)w.tok * half;
+            rotate(y, c, cosines + off, sines + off, a.interleaved, 1.f);
+            if (live) Vec8<E>::store(a.out[w.z], (rows.t0 + w.tok) * a.out_stride[w.z] + w.off, c, y);
         }
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
-        const float rms = rsqrtf(group_sum<LPR>(ss) * (1.f / D) + a.eps);
-        const float *wt = a.w[w.z];
-        if (wt) {
-            float wv[8];
-            load8(wt + 8 * l, wv);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= rms * wv[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= rms;
-        }
-        const int off = (int)w.tok * half;
-        rotate<LPR>(y, l, cosines + off, sines + off, a.rot, a.interleaved, 1.f);
-        if (live) Vec8<E>::store(a.out[w.z], (rows.t0 + w.tok) * a.out_stride[w.z] + w.off, y);
     }
 }
 
-// Persistent: CTA b takes row blocks b, b + grid, ...; each lane keeps its 8
-// columns of both weight gradients in registers, summed over the CTA at the
-// end and over the CTAs by a second kernel (a fixed order, no atomics).
+// Persistent: CTA b takes the rows of blocks b, b + grid, ... (each a.blocks
+// blocks, as above); each lane keeps its 8 columns of both weight gradients in
+// registers, summed over the CTA at the end and over the CTAs by a second kernel
+// (a fixed order, no atomics).
 template <class E, int D, int kIter>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(E) == 2 ? 3 : 2)
     gdn_qk_norm_rope_backward_kernel(const __grid_constant__ RopeArgs a) {
     extern __shared__ __align__(16) float smem[];
-    constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
+    constexpr int LPR = D / 8, GROUPS = kThreads / LPR, kBlock = GROUPS * kIter;
     const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+    const Pieces c(l, a.rot, a.interleaved);
     const int half = a.rot / 2;
-    float acc[2][8];
+    float2 acc[2][4];
 #pragma unroll
     for (int z = 0; z < 2; ++z)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[z][j] = 0.f;
-    for (int64_t first = (int64_t)blockIdx.x * (GROUPS * kIter); first < a.rows;
-         first += (int64_t)gridDim.x * (GROUPS * kIter)) {
-        const Rows rows(a, first, GROUPS * kIter);
-        Vec8<E> x[kIter], g[kIter];
+        for (int j = 0; j < 4; ++j) acc[z][j] = splat(0.f);
+    const int64_t per = (int64_t)kBlock * a.blocks;
+    for (int64_t first = blockIdx.x * per; first < a.rows; first += gridDim.x * per) {
+        const Rows rows(a, first, (int)per);
+        Vec8<E> next_x[kIter], next_g[kIter];
+        auto load = [&](uint32_t r0) {
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-            const uint32_t r = i * GROUPS + grp;
-            if (r < rows.n) {
-                const Row<D> w(a, rows, r, l);
-                x[i].load(a.x[w.z], (rows.t0 + w.tok) * a.x_stride[w.z] + w.off);
-                g[i].load(a.dz[w.z], (rows.t0 + w.tok) * a.dz_stride[w.z] + w.off);
+            for (int i = 0; i < kIter; ++i) {
+                const uint32_t r = r0 + i * GROUPS;
+                if (r < rows.n) {
+                    const Row<D> w(a, rows, r);
+                    next_x[i].load(a.x[w.z], (rows.t0 + w.tok) * a.x_stride[w.z] + w.off, c);
+                    next_g[i].load(a.dz[w.z], (rows.t0 + w.tok) * a.dz_stride[w.z] + w.off, c);
+                }
             }
-        }
-        __syncthreads();  // the previous block's angles have been read
+        };
+        load(grp);
+        __syncthreads();  // the previous rows' angles have been read
         float *cosines = smem, *sines = smem + rows.n_tok * half;
-        angles(a, rows.t0, (int)rows.n_tok, cosines, sines);
+        angles(a, rows.t0, rows.n_tok, cosines, sines);
         __syncthreads();
+        for (uint32_t b0 = 0; b0 < rows.n; b0 += kBlock) {
+            Vec8<E> x[kIter], g[kIter];
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-            const uint32_t r = i * GROUPS + grp;
-            const bool live = r < rows.n;
-            const Row<D> w(a, rows, live ? r : 0, l);
-            float n[8], dy[8];
-            if (live) {
+            for (int i = 0; i < kIter; ++i) {
+                x[i] = next_x[i];
+                g[i] = next_g[i];
+            }
+            load(b0 + kBlock + grp);
+#pragma unroll
+            for (int i = 0; i < kIter; ++i) {
+                const uint32_t r = b0 + i * GROUPS + grp;
+                const bool live = r < rows.n;  // every lane runs the shuffles
+                const Row<D> w(a, rows, live ? r : 0);
+                float2 n[4], dy[4];
                 x[i].get(n);
                 g[i].get(dy);
-            } else {
+                const float rms = rsqrtf(group_sum<LPR>(dot8(n, n)) * (1.f / D) + a.eps);
+                const int off = (int)w.tok * half;
+                rotate(dy, c, cosines + off, sines + off, a.interleaved, -1.f);
+                float2 wv[4];
+                if (a.w[w.z]) {
+                    load_pieces(a.w[w.z], c, wv);
+                } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) n[j] = dy[j] = 0.f;
+                    for (int j = 0; j < 4; ++j) wv[j] = splat(1.f);
+                }
+                // selected, not multiplied by 0 or 1: a key's infinity stays the key's
+                const bool to_q = live && !w.z, to_k = live && w.z;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    n[j] = fmul2(n[j], splat(rms));
+                    const float2 dn = fmul2(dy[j], n[j]);
+                    acc[0][j].x += to_q ? dn.x : 0.f;
+                    acc[0][j].y += to_q ? dn.y : 0.f;
+                    acc[1][j].x += to_k ? dn.x : 0.f;
+                    acc[1][j].y += to_k ? dn.y : 0.f;
+                    dy[j] = fmul2(dy[j], wv[j]);
+                }
+                const float2 dot = splat(-group_sum<LPR>(dot8(dy, n)) * (1.f / D));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) dy[j] = fmul2(ffma2(n[j], dot, dy[j]), splat(rms));
+                if (live) Vec8<E>::store(a.out[w.z], (rows.t0 + w.tok) * a.out_stride[w.z] + w.off, c, dy);
             }
-            float ss = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(n[j], n[j], ss);
-            const float rms = rsqrtf(group_sum<LPR>(ss) * (1.f / D) + a.eps);
-            const int off = (int)w.tok * half;
-            rotate<LPR>(dy, l, cosines + off, sines + off, a.rot, a.interleaved, -1.f);
-            float wv[8];
-            if (a.w[w.z]) {
-                load8(a.w[w.z] + 8 * l, wv);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) wv[j] = 1.f;
-            }
-            float dot = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                n[j] *= rms;
-                const float dn = dy[j] * n[j];  // a dead row's is 0 times 0
-                acc[0][j] += w.z ? 0.f : dn;
-                acc[1][j] += w.z ? dn : 0.f;
-                dy[j] *= wv[j];
-                dot = fmaf(dy[j], n[j], dot);
-            }
-            dot = group_sum<LPR>(dot) * (1.f / D);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) dy[j] = rms * (dy[j] - n[j] * dot);
-            if (live) Vec8<E>::store(a.out[w.z], (rows.t0 + w.tok) * a.out_stride[w.z] + w.off, dy);
         }
     }
     if (!a.dw_part) return;
@@ -316,8 +350,9 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) smem[grp * D + 8 * l + j] = acc[z][j];
+        float *mine = smem + grp * D;
+        *reinterpret_cast<float4 *>(mine + c.p0) = make_float4(acc[z][0].x, acc[z][0].y, acc[z][1].x, acc[z][1].y);
+        *reinterpret_cast<float4 *>(mine + c.p1) = make_float4(acc[z][2].x, acc[z][2].y, acc[z][3].x, acc[z][3].y);
         __syncthreads();
         for (int d = threadIdx.x; d < D; d += kThreads) {
             float s = 0.f;
@@ -345,38 +380,41 @@ bool supported(int32_t D) { return D == 16 || D == 32 || D == 64 || D == 128 || 
 // Tokens a block of `rows` consecutive rows can touch.
 int64_t tokens_of(int64_t rows, int32_t H) { return rows / H + 2; }
 
+// Blocks of `block` rows per CTA, so that their angles are computed once: as many
+// (up to `most`) as keep `ctas` CTAs busy and the angles within 40 KB.
+int blocks_per_cta(const RopeArgs &a, int64_t block, int64_t ctas, int most) {
+    int n = 1;
+    while (n < most && a.rows >= block * 2 * n * ctas &&
+           tokens_of(block * 2 * n, a.H) * a.rot * (int64_t)sizeof(float) <= 40 * 1024)
+        n *= 2;
+    return n;
+}
+
 template <class E, int D>
-cudaError_t launch_forward(const RopeArgs &a, cudaStream_t s) {
+cudaError_t launch_forward(RopeArgs a, cudaStream_t s) {
     constexpr int GROUPS = kThreads / (D / 8);
-    // four rows per lane group once that still fills the GPU: their loads
-    // overlap and the angles are shared; one row each below that (latency)
-    const bool many = a.rows >= (int64_t)GROUPS * 4 * 592;
-    const int iter = many ? 4 : 1;
-    const int64_t blocks = (a.rows + GROUPS * iter - 1) / (GROUPS * iter);
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const size_t smem = (size_t)tokens_of(GROUPS * iter, a.H) * a.rot * sizeof(float);
-    auto *fn = many ? gdn_qk_norm_rope_kernel<E, D, 4> : gdn_qk_norm_rope_kernel<E, D, 1>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    fn<<<(unsigned)blocks, kThreads, smem, s>>>(a);
+    // two rows per lane group at a time once that still fills the GPU, one below (latency)
+    const bool many = a.rows >= (int64_t)GROUPS * 2 * 592;
+    const int block = GROUPS * (many ? 2 : 1);
+    a.blocks = many ? blocks_per_cta(a, block, 592, 8) : 1;
+    const int64_t per = (int64_t)block * a.blocks, ctas = (a.rows + per - 1) / per;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const size_t smem = (size_t)tokens_of(per, a.H) * a.rot * sizeof(float);
+    auto *fn = many ? gdn_qk_norm_rope_kernel<E, D, 2> : gdn_qk_norm_rope_kernel<E, D, 1>;
+    fn<<<(unsigned)ctas, kThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
 template <class E, int D>
-cudaError_t launch_backward(const RopeArgs &a, float *dwq, float *dwk, cudaStream_t s) {
-    constexpr int GROUPS = kThreads / (D / 8), kIter = sizeof(E) == 2 ? 4 : 2;
-    const int64_t blocks = (a.rows + GROUPS * kIter - 1) / (GROUPS * kIter);
-    const int ctas = (int)(blocks < kBackwardCtas ? blocks : kBackwardCtas);
-    size_t smem = (size_t)tokens_of(GROUPS * kIter, a.H) * a.rot * sizeof(float);
+cudaError_t launch_backward(RopeArgs a, float *dwq, float *dwk, cudaStream_t s) {
+    constexpr int GROUPS = kThreads / (D / 8), kIter = 2;
+    const int block = GROUPS * kIter;
+    a.blocks = blocks_per_cta(a, block, kBackwardCtas, 8);
+    const int64_t per = (int64_t)block * a.blocks, want = (a.rows + per - 1) / per;
+    const int ctas = (int)(want < kBackwardCtas ? want : kBackwardCtas);
+    size_t smem = (size_t)tokens_of(per, a.H) * a.rot * sizeof(float);
     if (smem < (size_t)GROUPS * D * sizeof(float)) smem = (size_t)GROUPS * D * sizeof(float);
-    auto *fn = gdn_qk_norm_rope_backward_kernel<E, D, kIter>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    fn<<<ctas, kThreads, smem, s>>>(a);
+    gdn_qk_norm_rope_backward_kernel<E, D, kIter><<<ctas, kThreads, smem, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.dw_part) return e;
     gdn_qk_norm_dw_kernel<<<(2 * D * 32 + 255) / 256, 256, 0, s>>>(a.dw_part, ctas, D, dwq, dwk);
@@ -424,12 +462,16 @@ gdn_status common(RopeArgs &a, const void *xq, const void *xk, gdn_dtype dt, int
     const int64_t esz = dt == GDN_DTYPE_BF16 ? 2 : 4;
     if (xq_stride < (int64_t)Hq * D || (Hk > 0 && xk_stride < (int64_t)Hk * D)) return GDN_ERR_INVALID_ARGUMENT;
     if ((xq_stride * esz) % 16 || (Hk > 0 && (xk_stride * esz) % 16)) return GDN_ERR_INVALID_ARGUMENT;
-    if (!supported(D) || rot % 16 != 0) return GDN_ERR_UNSUPPORTED;
+    if (!supported(D) || rot % 16 != 0 || Hq > 32768 - Hk) return GDN_ERR_UNSUPPORTED;
     a.x[0] = xq; a.x[1] = xk;
     a.w[0] = wq; a.w[1] = wk;
     a.x_stride[0] = xq_stride; a.x_stride[1] = xk_stride;
     a.pos = positions; a.inv_freq = inv_freq; a.eps = eps;
-    a.Hq = Hq; a.H = Hq + Hk; a.rot = rot; a.interleaved = interleaved;
+    a.Hq = Hq; a.H = Hq + Hk;
+    auto inverse = [](uint32_t n) { return (uint32_t)((((uint64_t)1 << 32) + n - 1) / n); };
+    a.inv_h = inverse((uint32_t)a.H);
+    a.inv_half = rot > 0 ? inverse((uint32_t)rot / 2) : 0;
+    a.rot = rot; a.interleaved = interleaved;
     a.T = T; a.rows = T * (int64_t)(Hq + Hk);
     return a.rows > ((int64_t)1 << 33) ? GDN_ERR_UNSUPPORTED : GDN_OK;  // the grid's x dimension
 }

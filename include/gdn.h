@@ -675,7 +675,7 @@ GDN_API gdn_status gdn_linear_decode_step_slots(const void *q, const void *k, co
  *                       1: (y[2i], y[2i + 1]).
  *   q, k                outputs [T][Hq][D], [T][Hk][D] io_dtype, contiguous;
  *                       computed in fp32, rounded once.
- * Supported: D in {16, 32, 64, 128, 256}, either dtype.
+ * Supported: D in {16, 32, 64, 128, 256}, Hq + Hk <= 32768, either dtype.
  */
 GDN_API gdn_status gdn_qk_norm_rope(const void *xq, const void *xk, gdn_dtype io_dtype,
                                     int64_t xq_stride, int64_t xk_stride, const float *wq,

@@ -131,7 +131,8 @@ ROPE_BAD = [(dict(xq=None), INVALID), (dict(xk=None), INVALID), (dict(xq=MIS), I
             (dict(axes=5, sections=[8, 8, 8, 4, 4]), UNSUPPORTED), (dict(rot=-16), INVALID),
             (dict(rot=272), INVALID), (dict(rot=24), UNSUPPORTED), (dict(inter=2), INVALID),
             (dict(sq=24 * 256 - 8), INVALID), (dict(sq=24 * 256 + 4), INVALID), (dict(Hq=0), INVALID),
-            (dict(Hk=-1), INVALID), (dict(D=96, rot=96), UNSUPPORTED), (dict(T=-1), INVALID)]
+            (dict(Hk=-1), INVALID), (dict(D=96, rot=96), UNSUPPORTED), (dict(T=-1), INVALID),
+            (dict(Hq=32768, sq=32768 * 256), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("kw,code", ROPE_BAD + [(dict(q=None), INVALID), (dict(k=None), INVALID),
