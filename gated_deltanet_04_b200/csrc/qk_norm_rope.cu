@@ -31,23 +31,32 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxAxes = 4;
-constexpr int kBackwardCtas = 592;  // persistent grid of the backward pass (4 per SM of 148)
+constexpr int kBackwardCtas = 444;  // persistent grid of the backward pass (3 per SM of 148)
+
+// The queries or the keys: a CTA works on one side only, so that its heads,
+// weights and pointers are uniform.
+struct Side {
+    const void *x, *dz;        // inputs; backward: gradients of the outputs
+    void *out;                 // outputs, or the gradients of x
+    const float *w;            // [D] or null (ones)
+    uint32_t x_step, out_step, dz_step;  // bytes per token
+    int32_t H;
+    uint32_t inv_h;            // ceil(2^32 / H) (H > 1)
+    int64_t rows;              // T * H
+    uint32_t ctas;
+};
 
 struct RopeArgs {
-    const void *x[2];          // q, k inputs
-    const void *dz[2];         // backward: gradients of the outputs
-    void *out[2];              // outputs, or the gradients of x
-    const float *w[2];         // [D] or null (ones)
-    float *dw_part;            // backward: [CTAs][2][D] or null
-    int64_t x_stride[2], out_stride[2], dz_stride[2];  // elements per token
+    Side side[2];
+    float *dw_part;            // backward: [CTAs][D] or null
     const int32_t *pos;        // [axes][T]
     const float *inv_freq;     // [rot / 2]
     int32_t last[kMaxAxes];    // frequency i belongs to the first axis with i < last[axis]
     float eps;
-    int32_t Hq, H, rot, interleaved;
-    uint32_t inv_h, inv_half;  // ceil(2^32 / H) (H > 1), ceil(2^32 / (rot / 2))
+    int32_t rot, interleaved;
+    uint32_t inv_half;         // ceil(2^32 / (rot / 2))
     int32_t blocks;            // blocks of kIter rows per lane group that share their angles
-    int64_t T, rows;           // rows = T * H
+    int64_t T;
 };
 
 using sm100::ffma2;
@@ -75,9 +84,9 @@ struct Vec8;
 template <>
 struct Vec8<__nv_bfloat16> {
     uint2 a, b;
-    __device__ __forceinline__ void load(const void *p, int64_t i, const Pieces &c) {
-        a = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i + c.p0);
-        b = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i + c.p1);
+    __device__ __forceinline__ void load(const uint8_t *p, const Pieces &c) {
+        a = *reinterpret_cast<const uint2 *>(p + 2 * c.p0);
+        b = *reinterpret_cast<const uint2 *>(p + 2 * c.p1);
     }
     static __device__ __forceinline__ float2 wide(uint32_t w) {
         return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -92,17 +101,17 @@ struct Vec8<__nv_bfloat16> {
         const __nv_bfloat162 t = __floats2bfloat162_rn(x.x, x.y);
         return *reinterpret_cast<const uint32_t *>(&t);
     }
-    static __device__ __forceinline__ void store(void *p, int64_t i, const Pieces &c, const float2 (&f)[4]) {
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p) + i + c.p0) = make_uint2(narrow(f[0]), narrow(f[1]));
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p) + i + c.p1) = make_uint2(narrow(f[2]), narrow(f[3]));
+    static __device__ __forceinline__ void store(uint8_t *p, const Pieces &c, const float2 (&f)[4]) {
+        *reinterpret_cast<uint2 *>(p + 2 * c.p0) = make_uint2(narrow(f[0]), narrow(f[1]));
+        *reinterpret_cast<uint2 *>(p + 2 * c.p1) = make_uint2(narrow(f[2]), narrow(f[3]));
     }
 };
 template <>
 struct Vec8<float> {
     float4 a, b;
-    __device__ __forceinline__ void load(const void *p, int64_t i, const Pieces &c) {
-        a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + c.p0);
-        b = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + c.p1);
+    __device__ __forceinline__ void load(const uint8_t *p, const Pieces &c) {
+        a = *reinterpret_cast<const float4 *>(p + 4 * c.p0);
+        b = *reinterpret_cast<const float4 *>(p + 4 * c.p1);
     }
     __device__ __forceinline__ void get(float2 (&f)[4]) const {
         f[0] = make_float2(a.x, a.y);
@@ -110,9 +119,9 @@ struct Vec8<float> {
         f[2] = make_float2(b.x, b.y);
         f[3] = make_float2(b.z, b.w);
     }
-    static __device__ __forceinline__ void store(void *p, int64_t i, const Pieces &c, const float2 (&f)[4]) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(p) + i + c.p0) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-        *reinterpret_cast<float4 *>(static_cast<float *>(p) + i + c.p1) = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+    static __device__ __forceinline__ void store(uint8_t *p, const Pieces &c, const float2 (&f)[4]) {
+        *reinterpret_cast<float4 *>(p + 4 * c.p0) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+        *reinterpret_cast<float4 *>(p + 4 * c.p1) = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
     }
 };
 
@@ -180,31 +189,32 @@ __device__ __forceinline__ float dot8(const float2 (&a)[4], const float2 (&b)[4]
     return s.x + s.y;
 }
 
-// A CTA's rows: `first` and the following ones, as tokens and heads.
+// A CTA's rows of its side: `first` and the following ones, as tokens and heads.
 struct Rows {
     int64_t t0;     // token of the first row
     uint32_t h0;    // its head
     uint32_t n;     // rows
     uint32_t n_tok;
-    __device__ __forceinline__ Rows(const RopeArgs &a, int64_t first, int per) {
+    __device__ __forceinline__ Rows(const Side &d, int64_t first, int per) {
         // (a 64-bit division only where 32 bits do not hold the row)
-        t0 = a.rows >> 32 ? first / a.H : (int64_t)((uint32_t)first / (uint32_t)a.H);
-        h0 = (uint32_t)(first - t0 * a.H);
-        n = (uint32_t)(a.rows - first < per ? a.rows - first : per);
-        n_tok = (h0 + n - 1) / (uint32_t)a.H + 1;
+        t0 = d.rows >> 32 ? first / d.H : (int64_t)((uint32_t)first / (uint32_t)d.H);
+        h0 = (uint32_t)(first - t0 * d.H);
+        n = (uint32_t)(d.rows - first < per ? d.rows - first : per);
+        n_tok = (h0 + n - 1) / (uint32_t)d.H + 1;
     }
 };
-// Row r of them: its token (from t0), whether it is a key's, its offset within the token.
-template <int D>
+// Row r of them: its token (from t0) and its head.
 struct Row {
-    uint32_t tok;
-    int z, off;
-    __device__ __forceinline__ Row(const RopeArgs &a, const Rows &rows, uint32_t r) {
+    uint32_t tok, h;
+    __device__ __forceinline__ Row(const Side &d, const Rows &rows, uint32_t r) {
         const uint32_t x = rows.h0 + r;  // x H < 2^32: the product with ceil(2^32 / H) divides exactly
-        tok = a.H == 1 ? x : __umulhi(x, a.inv_h);
-        const int h = (int)(x - tok * (uint32_t)a.H);
-        z = h >= a.Hq;
-        off = (h - (z ? a.Hq : 0)) * D;
+        tok = d.H == 1 ? x : __umulhi(x, d.inv_h);
+        h = x - tok * (uint32_t)d.H;
+    }
+    // from a pointer to token t0
+    template <class E, int D, class P>
+    __device__ __forceinline__ P *at(P *base, uint32_t step) const {
+        return base + (uint64_t)tok * step + h * (uint32_t)(D * sizeof(E));
     }
 };
 
@@ -216,20 +226,23 @@ __global__ void __launch_bounds__(kThreads) gdn_qk_norm_rope_kernel(const __grid
     extern __shared__ __align__(16) float smem[];
     constexpr int LPR = D / 8, GROUPS = kThreads / LPR, kBlock = GROUPS * kIter;
     const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+    const bool key = blockIdx.x >= a.side[0].ctas;
+    const Side &d = a.side[key];
     const Pieces c(l, a.rot, a.interleaved);
-    const Rows rows(a, (int64_t)blockIdx.x * (kBlock * a.blocks), kBlock * a.blocks);
+    const Rows rows(d, (int64_t)(blockIdx.x - (key ? a.side[0].ctas : 0u)) * (kBlock * a.blocks), kBlock * a.blocks);
+    const uint8_t *in = static_cast<const uint8_t *>(d.x) + rows.t0 * d.x_step;
+    uint8_t *out = static_cast<uint8_t *>(d.out) + rows.t0 * d.out_step;
     Vec8<E> next[kIter];
     auto load = [&](uint32_t r0) {
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
             const uint32_t r = r0 + i * GROUPS;
-            if (r < rows.n) {
-                const Row<D> w(a, rows, r);
-                next[i].load(a.x[w.z], (rows.t0 + w.tok) * a.x_stride[w.z] + w.off, c);
-            }
+            if (r < rows.n) next[i].load(Row(d, rows, r).at<E, D>(in, d.x_step), c);
         }
     };
     load(grp);
+    float2 wv[4] = {splat(1.f), splat(1.f), splat(1.f), splat(1.f)};
+    if (d.w) load_pieces(d.w, c, wv);
     const int half = a.rot / 2;
     float *cosines = smem, *sines = smem + rows.n_tok * half;
     angles(a, rows.t0, rows.n_tok, cosines, sines);
@@ -243,55 +256,51 @@ __global__ void __launch_bounds__(kThreads) gdn_qk_norm_rope_kernel(const __grid
         for (int i = 0; i < kIter; ++i) {
             const uint32_t r = b0 + i * GROUPS + grp;
             const bool live = r < rows.n;  // every lane runs the shuffles
-            const Row<D> w(a, rows, live ? r : 0);
+            const Row w(d, rows, live ? r : 0);
             float2 y[4];
             x[i].get(y);
             const float2 rms = splat(rsqrtf(group_sum<LPR>(dot8(y, y)) * (1.f / D) + a.eps));
-            if (a.w[w.z]) {
-                float2 wv[4];
-                load_pieces(a.w[w.z], c, wv);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = fmul2(y[j], fmul2(rms, wv[j]));
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = fmul2(y[j], rms);
-            }
+            for (int j = 0; j < 4; ++j) y[j] = fmul2(y[j], fmul2(rms, wv[j]));
             const int off = (int)w.tok * half;
             rotate(y, c, cosines + off, sines + off, a.interleaved, 1.f);
-            if (live) Vec8<E>::store(a.out[w.z], (rows.t0 + w.tok) * a.out_stride[w.z] + w.off, c, y);
+            if (live) Vec8<E>::store(w.at<E, D>(out, d.out_step), c, y);
         }
     }
 }
 
-// Persistent: CTA b takes the rows of blocks b, b + grid, ... (each a.blocks
-// blocks, as above); each lane keeps its 8 columns of both weight gradients in
-// registers, summed over the CTA at the end and over the CTAs by a second kernel
-// (a fixed order, no atomics).
+// Persistent: a side's CTA b takes the rows of blocks b, b + ctas, ... (each
+// a.blocks blocks, as above); each lane keeps its 8 columns of the weight's
+// gradient in registers, summed over the CTA at the end and over the CTAs by a
+// second kernel (a fixed order, no atomics).
 template <class E, int D, int kIter>
 __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 ? 3 : 2)
     gdn_qk_norm_rope_backward_kernel(const __grid_constant__ RopeArgs a) {
     extern __shared__ __align__(16) float smem[];
     constexpr int LPR = D / 8, GROUPS = kThreads / LPR, kBlock = GROUPS * kIter;
     const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+    const bool key = blockIdx.x >= a.side[0].ctas;
+    const Side &d = a.side[key];
     const Pieces c(l, a.rot, a.interleaved);
     const int half = a.rot / 2;
-    float2 acc[2][4];
-#pragma unroll
-    for (int z = 0; z < 2; ++z)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[z][j] = splat(0.f);
+    float2 acc[4] = {splat(0.f), splat(0.f), splat(0.f), splat(0.f)};
+    float2 wv[4] = {splat(1.f), splat(1.f), splat(1.f), splat(1.f)};
+    if (d.w) load_pieces(d.w, c, wv);
     const int64_t per = (int64_t)kBlock * a.blocks;
-    for (int64_t first = blockIdx.x * per; first < a.rows; first += gridDim.x * per) {
-        const Rows rows(a, first, (int)per);
+    for (int64_t first = (blockIdx.x - (key ? a.side[0].ctas : 0u)) * per; first < d.rows; first += d.ctas * per) {
+        const Rows rows(d, first, (int)per);
+        const uint8_t *in = static_cast<const uint8_t *>(d.x) + rows.t0 * d.x_step;
+        const uint8_t *grad = static_cast<const uint8_t *>(d.dz) + rows.t0 * d.dz_step;
+        uint8_t *out = static_cast<uint8_t *>(d.out) + rows.t0 * d.out_step;
         Vec8<E> next_x[kIter], next_g[kIter];
         auto load = [&](uint32_t r0) {
 #pragma unroll
             for (int i = 0; i < kIter; ++i) {
                 const uint32_t r = r0 + i * GROUPS;
                 if (r < rows.n) {
-                    const Row<D> w(a, rows, r);
-                    next_x[i].load(a.x[w.z], (rows.t0 + w.tok) * a.x_stride[w.z] + w.off, c);
-                    next_g[i].load(a.dz[w.z], (rows.t0 + w.tok) * a.dz_stride[w.z] + w.off, c);
+                    const Row w(d, rows, r);
+                    next_x[i].load(w.at<E, D>(in, d.x_step), c);
+                    next_g[i].load(w.at<E, D>(grad, d.dz_step), c);
                 }
             }
         };
@@ -312,66 +321,61 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 ? 3 : 2)
             for (int i = 0; i < kIter; ++i) {
                 const uint32_t r = b0 + i * GROUPS + grp;
                 const bool live = r < rows.n;  // every lane runs the shuffles
-                const Row<D> w(a, rows, live ? r : 0);
+                const Row w(d, rows, live ? r : 0);
                 float2 n[4], dy[4];
                 x[i].get(n);
                 g[i].get(dy);
                 const float rms = rsqrtf(group_sum<LPR>(dot8(n, n)) * (1.f / D) + a.eps);
                 const int off = (int)w.tok * half;
                 rotate(dy, c, cosines + off, sines + off, a.interleaved, -1.f);
-                float2 wv[4];
-                if (a.w[w.z]) {
-                    load_pieces(a.w[w.z], c, wv);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) wv[j] = splat(1.f);
-                }
-                // selected, not multiplied by 0 or 1: a key's infinity stays the key's
-                const bool to_q = live && !w.z, to_k = live && w.z;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     n[j] = fmul2(n[j], splat(rms));
-                    const float2 dn = fmul2(dy[j], n[j]);
-                    acc[0][j].x += to_q ? dn.x : 0.f;
-                    acc[0][j].y += to_q ? dn.y : 0.f;
-                    acc[1][j].x += to_k ? dn.x : 0.f;
-                    acc[1][j].y += to_k ? dn.y : 0.f;
+                    if (live) acc[j] = ffma2(dy[j], n[j], acc[j]);
                     dy[j] = fmul2(dy[j], wv[j]);
                 }
                 const float2 dot = splat(-group_sum<LPR>(dot8(dy, n)) * (1.f / D));
 #pragma unroll
                 for (int j = 0; j < 4; ++j) dy[j] = fmul2(ffma2(n[j], dot, dy[j]), splat(rms));
-                if (live) Vec8<E>::store(a.out[w.z], (rows.t0 + w.tok) * a.out_stride[w.z] + w.off, c, dy);
+                if (live) Vec8<E>::store(w.at<E, D>(out, d.out_step), c, dy);
             }
         }
     }
     if (!a.dw_part) return;
-    // sum over the CTA's lane groups: [2][D] from GROUPS partials, in order
+    // sum over the CTA's lane groups: [D] from GROUPS partials, in order
     __syncthreads();
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-        float *mine = smem + grp * D;
-        *reinterpret_cast<float4 *>(mine + c.p0) = make_float4(acc[z][0].x, acc[z][0].y, acc[z][1].x, acc[z][1].y);
-        *reinterpret_cast<float4 *>(mine + c.p1) = make_float4(acc[z][2].x, acc[z][2].y, acc[z][3].x, acc[z][3].y);
-        __syncthreads();
-        for (int d = threadIdx.x; d < D; d += kThreads) {
-            float s = 0.f;
-            for (int q = 0; q < GROUPS; ++q) s += smem[q * D + d];
-            a.dw_part[((int64_t)blockIdx.x * 2 + z) * D + d] = s;
-        }
-        __syncthreads();
+    float *mine = smem + grp * D;
+    *reinterpret_cast<float4 *>(mine + c.p0) = make_float4(acc[0].x, acc[0].y, acc[1].x, acc[1].y);
+    *reinterpret_cast<float4 *>(mine + c.p1) = make_float4(acc[2].x, acc[2].y, acc[3].x, acc[3].y);
+    __syncthreads();
+    for (int i = threadIdx.x; i < D; i += kThreads) {
+        float s = 0.f;
+        for (int q = 0; q < GROUPS; ++q) s += smem[q * D + i];
+        a.dw_part[(int64_t)blockIdx.x * D + i] = s;
     }
 }
 
-// dw[z][d] = sum over CTAs of part[cta][z][d]: a warp per column.
-__global__ void gdn_qk_norm_dw_kernel(const float *part, int ctas, int D, float *dwq, float *dwk) {
-    const int col = (blockIdx.x * blockDim.x + threadIdx.x) / 32, lane = threadIdx.x & 31;
-    if (col >= 2 * D) return;
+// A side's dw[d] = the sum over its CTAs of part[cta][d]: 32 columns a CTA, 8 warps
+// over the rows, then the warps' sums in order.
+__global__ void gdn_qk_norm_dw_kernel(const float *part, uint32_t ctas_q, uint32_t ctas_k, int D, float *dwq,
+                                      float *dwk) {
+    __shared__ float sums[8][32];
+    const bool key = blockIdx.y;
+    float *dst = key ? dwk : dwq;
+    if (!dst) return;
+    const uint32_t first = key ? ctas_q : 0, n = key ? ctas_k : ctas_q;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = blockIdx.x * 32 + lane;
     float s = 0.f;
-    for (int c = lane; c < ctas; c += 32) s += part[(int64_t)c * 2 * D + col];
-    s = group_sum<32>(s);
-    float *dst = col < D ? dwq : dwk;
-    if (lane == 0 && dst) dst[col < D ? col : col - D] = s;
+    if (d < D) {
+#pragma unroll 8
+        for (uint32_t c = warp; c < n; c += 8) s += part[(int64_t)(first + c) * D + d];
+    }
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && d < D) {
+        for (int w = 1; w < 8; ++w) s += sums[w][lane];
+        dst[d] = s;
+    }
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -381,27 +385,34 @@ bool supported(int32_t D) { return D == 16 || D == 32 || D == 64 || D == 128 || 
 int64_t tokens_of(int64_t rows, int32_t H) { return rows / H + 2; }
 
 // Blocks of `block` rows per CTA, so that their angles are computed once: as many
-// (up to `most`) as keep `ctas` CTAs busy and the angles within 40 KB.
-int blocks_per_cta(const RopeArgs &a, int64_t block, int64_t ctas, int most) {
+// (up to 8) as keep `ctas` CTAs busy and the angles within 40 KB.
+int blocks_per_cta(const RopeArgs &a, int64_t block, int64_t ctas) {
+    const int64_t rows = a.side[0].rows + a.side[1].rows;
+    const int32_t fewest = a.side[1].H > 0 && a.side[1].H < a.side[0].H ? a.side[1].H : a.side[0].H;
     int n = 1;
-    while (n < most && a.rows >= block * 2 * n * ctas &&
-           tokens_of(block * 2 * n, a.H) * a.rot * (int64_t)sizeof(float) <= 40 * 1024)
+    while (n < 8 && rows >= block * 2 * n * ctas &&
+           tokens_of(block * 2 * n, fewest) * a.rot * (int64_t)sizeof(float) <= 40 * 1024)
         n *= 2;
     return n;
+}
+
+// Shared memory for the angles of `per` rows of either side.
+size_t angle_bytes(const RopeArgs &a, int64_t per) {
+    const int32_t fewest = a.side[1].H > 0 && a.side[1].H < a.side[0].H ? a.side[1].H : a.side[0].H;
+    return (size_t)tokens_of(per, fewest) * a.rot * sizeof(float);
 }
 
 template <class E, int D>
 cudaError_t launch_forward(RopeArgs a, cudaStream_t s) {
     constexpr int GROUPS = kThreads / (D / 8);
     // two rows per lane group at a time once that still fills the GPU, one below (latency)
-    const bool many = a.rows >= (int64_t)GROUPS * 2 * 592;
+    const bool many = a.side[0].rows + a.side[1].rows >= (int64_t)GROUPS * 2 * 592;
     const int block = GROUPS * (many ? 2 : 1);
-    a.blocks = many ? blocks_per_cta(a, block, 592, 8) : 1;
-    const int64_t per = (int64_t)block * a.blocks, ctas = (a.rows + per - 1) / per;
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const size_t smem = (size_t)tokens_of(per, a.H) * a.rot * sizeof(float);
+    a.blocks = many ? blocks_per_cta(a, block, 592) : 1;
+    const int64_t per = (int64_t)block * a.blocks;
+    for (Side &d : a.side) d.ctas = (uint32_t)((d.rows + per - 1) / per);
     auto *fn = many ? gdn_qk_norm_rope_kernel<E, D, 2> : gdn_qk_norm_rope_kernel<E, D, 1>;
-    fn<<<(unsigned)ctas, kThreads, smem, s>>>(a);
+    fn<<<a.side[0].ctas + a.side[1].ctas, kThreads, angle_bytes(a, per), s>>>(a);
     return cudaGetLastError();
 }
 
@@ -409,15 +420,21 @@ template <class E, int D>
 cudaError_t launch_backward(RopeArgs a, float *dwq, float *dwk, cudaStream_t s) {
     constexpr int GROUPS = kThreads / (D / 8), kIter = 2;
     const int block = GROUPS * kIter;
-    a.blocks = blocks_per_cta(a, block, kBackwardCtas, 8);
-    const int64_t per = (int64_t)block * a.blocks, want = (a.rows + per - 1) / per;
-    const int ctas = (int)(want < kBackwardCtas ? want : kBackwardCtas);
-    size_t smem = (size_t)tokens_of(per, a.H) * a.rot * sizeof(float);
+    a.blocks = blocks_per_cta(a, block, kBackwardCtas);
+    const int64_t per = (int64_t)block * a.blocks;
+    // CTAs for each side in proportion to its rows (one at least), no more than it has blocks
+    const int64_t all = a.side[0].rows + a.side[1].rows;
+    for (Side &d : a.side) {
+        const int64_t blocks = (d.rows + per - 1) / per, share = (kBackwardCtas - 1) * d.rows / all;
+        d.ctas = (uint32_t)(blocks < share ? blocks : share > 0 ? share : d.rows > 0);
+    }
+    size_t smem = angle_bytes(a, per);
     if (smem < (size_t)GROUPS * D * sizeof(float)) smem = (size_t)GROUPS * D * sizeof(float);
-    gdn_qk_norm_rope_backward_kernel<E, D, kIter><<<ctas, kThreads, smem, s>>>(a);
+    gdn_qk_norm_rope_backward_kernel<E, D, kIter><<<a.side[0].ctas + a.side[1].ctas, kThreads, smem, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.dw_part) return e;
-    gdn_qk_norm_dw_kernel<<<(2 * D * 32 + 255) / 256, 256, 0, s>>>(a.dw_part, ctas, D, dwq, dwk);
+    gdn_qk_norm_dw_kernel<<<dim3((D + 31) / 32, 2), 256, 0, s>>>(a.dw_part, a.side[0].ctas, a.side[1].ctas, D, dwq,
+                                                                dwk);
     return cudaGetLastError();
 }
 
@@ -463,17 +480,25 @@ gdn_status common(RopeArgs &a, const void *xq, const void *xk, gdn_dtype dt, int
     if (xq_stride < (int64_t)Hq * D || (Hk > 0 && xk_stride < (int64_t)Hk * D)) return GDN_ERR_INVALID_ARGUMENT;
     if ((xq_stride * esz) % 16 || (Hk > 0 && (xk_stride * esz) % 16)) return GDN_ERR_INVALID_ARGUMENT;
     if (!supported(D) || rot % 16 != 0 || Hq > 32768 - Hk) return GDN_ERR_UNSUPPORTED;
-    a.x[0] = xq; a.x[1] = xk;
-    a.w[0] = wq; a.w[1] = wk;
-    a.x_stride[0] = xq_stride; a.x_stride[1] = xk_stride;
-    a.pos = positions; a.inv_freq = inv_freq; a.eps = eps;
-    a.Hq = Hq; a.H = Hq + Hk;
+    // a token's bytes are 32-bit in the kernels
+    if (xq_stride > 0x3fffffff || (Hk > 0 && xk_stride > 0x3fffffff)) return GDN_ERR_UNSUPPORTED;
     auto inverse = [](uint32_t n) { return (uint32_t)((((uint64_t)1 << 32) + n - 1) / n); };
-    a.inv_h = inverse((uint32_t)a.H);
+    const int32_t heads[2] = {Hq, Hk};
+    for (int z = 0; z < 2; ++z) {
+        Side &d = a.side[z];
+        d.x = z ? xk : xq;
+        d.w = z ? wk : wq;
+        d.x_step = heads[z] ? (uint32_t)((z ? xk_stride : xq_stride) * esz) : 0;
+        d.H = heads[z];
+        d.inv_h = heads[z] > 1 ? inverse((uint32_t)heads[z]) : 0;
+        d.rows = T * (int64_t)heads[z];
+        d.dz_step = d.out_step = (uint32_t)(heads[z] * (int64_t)D * esz);
+    }
     a.inv_half = rot > 0 ? inverse((uint32_t)rot / 2) : 0;
+    a.pos = positions; a.inv_freq = inv_freq; a.eps = eps;
     a.rot = rot; a.interleaved = interleaved;
-    a.T = T; a.rows = T * (int64_t)(Hq + Hk);
-    return a.rows > ((int64_t)1 << 33) ? GDN_ERR_UNSUPPORTED : GDN_OK;  // the grid's x dimension
+    a.T = T;
+    return T * (int64_t)(Hq + Hk) > ((int64_t)1 << 33) ? GDN_ERR_UNSUPPORTED : GDN_OK;  // the grid's x dimension
 }
 
 }  // namespace
@@ -500,8 +525,8 @@ gdn_status gdn_qk_norm_rope(const void *xq, const void *xk, gdn_dtype io_dtype, 
         if ((q && q == i) || (k && k == i)) return GDN_ERR_INVALID_ARGUMENT;
     if (q && q == k) return GDN_ERR_INVALID_ARGUMENT;
     if (T == 0) return GDN_OK;
-    a.out[0] = q; a.out[1] = k;
-    a.out_stride[0] = (int64_t)Hq * D; a.out_stride[1] = (int64_t)Hk * D;
+    a.side[0].out = q;
+    a.side[1].out = k;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = io_dtype == GDN_DTYPE_BF16
                               ? gdn::dispatch<__nv_bfloat16>(a, D, false, nullptr, nullptr, s)
@@ -510,7 +535,7 @@ gdn_status gdn_qk_norm_rope(const void *xq, const void *xk, gdn_dtype io_dtype, 
 }
 
 size_t gdn_qk_norm_rope_backward_workspace_bytes(int32_t D) {
-    return gdn::supported(D) ? (size_t)gdn::kBackwardCtas * 2 * D * sizeof(float) : 0;
+    return gdn::supported(D) ? (size_t)gdn::kBackwardCtas * D * sizeof(float) : 0;
 }
 
 gdn_status gdn_qk_norm_rope_backward(const void *dq, const void *dk, const void *xq, const void *xk,
@@ -530,6 +555,7 @@ gdn_status gdn_qk_norm_rope_backward(const void *dq, const void *dk, const void 
     const int64_t esz = io_dtype == GDN_DTYPE_BF16 ? 2 : 4;
     if (dxq_stride < (int64_t)Hq * D || (Hk > 0 && dxk_stride < (int64_t)Hk * D)) return GDN_ERR_INVALID_ARGUMENT;
     if ((dxq_stride * esz) % 16 || (Hk > 0 && (dxk_stride * esz) % 16)) return GDN_ERR_INVALID_ARGUMENT;
+    if (dxq_stride > 0x3fffffff || (Hk > 0 && dxk_stride > 0x3fffffff)) return GDN_ERR_UNSUPPORTED;
     const void *all[] = {dq, dk, xq, xk, wq, wk, positions, inv_freq, dxq, dxk, dwq, dwk, workspace};
     for (const void *p : all)
         if (p && !gdn::aligned16(p)) return GDN_ERR_INVALID_ARGUMENT;
@@ -551,10 +577,12 @@ gdn_status gdn_qk_norm_rope_backward(const void *dq, const void *dk, const void 
             if (p && cudaMemsetAsync(p, 0, (size_t)D * sizeof(float), s) != cudaSuccess) return GDN_ERR_CUDA;
         return GDN_OK;
     }
-    a.dz[0] = dq; a.dz[1] = dk;
-    a.dz_stride[0] = (int64_t)Hq * D; a.dz_stride[1] = (int64_t)Hk * D;
-    a.out[0] = dxq; a.out[1] = dxk;
-    a.out_stride[0] = dxq_stride; a.out_stride[1] = dxk_stride;
+    a.side[0].dz = dq;
+    a.side[1].dz = dk;
+    a.side[0].out = dxq;
+    a.side[1].out = dxk;
+    a.side[0].out_step = (uint32_t)(dxq_stride * esz);
+    a.side[1].out_step = (uint32_t)(dxk_stride * esz);
     a.dw_part = weights ? static_cast<float *>(workspace) : nullptr;
     const cudaError_t e = io_dtype == GDN_DTYPE_BF16
                               ? gdn::dispatch<__nv_bfloat16>(a, D, true, dwq, dwk, s)

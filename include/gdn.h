@@ -660,7 +660,8 @@ GDN_API gdn_status gdn_linear_decode_step_slots(const void *q, const void *k, co
  *                       token; xq_stride, xk_stride are the elements from one
  *                       token to the next (Hq * D, Hk * D when packed; larger
  *                       when they are parts of one projection), a multiple of
- *                       16 bytes.  Hk may be 0 (xk, wk and k are then unused).
+ *                       16 bytes and below 2^30.  Hk may be 0 (xk, wk and k are
+ *                       then unused).
  *   wq, wk              fp32 [D] weights, or NULL for ones.
  *   eps                 > 0.
  *   positions           int32 [axes][T], any values; axes <= 4.
