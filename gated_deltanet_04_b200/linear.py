@@ -4,67 +4,102 @@ lam = exp(log_decay[h]).  Argument marshalling only, as the package's other
 calls.  log_decay is a constant of the layer: there is no gradient for it."""
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
-from . import DTYPE, GdnError, _check, _ptr, library
+from . import DTYPE, GdnError, _check, library
 
 F32, I32 = torch.float32, torch.int32
 
 
-@contextlib.contextmanager
-def _on(dev, stream):
-    """The device of the tensors and the stream of the call made current, so
-    that outputs and workspaces allocated for it belong to that stream; yields
-    the stream's handle."""
-    if stream is not None and stream.device != dev:
+def _need(t, name, shape, dtype, dev):
+    """_check without building its messages: these calls are made per token and
+    layer, and an elaborate check of every argument costs more than the launch."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != dev
+            or not t.is_contiguous()):
+        _check(t, name, shape, dtype, dev)
+
+
+def _at(t):
+    """The address of a tensor, or None."""
+    return None if t is None else t.data_ptr()
+
+
+def _run(dev, stream, call):
+    """call(handle) with the tensors' device and the call's stream current, so that
+    outputs and workspaces it allocates belong to that stream."""
+    if stream is None:
+        if torch.cuda.current_device() == dev.index:
+            return call(torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(dev):
+            return call(torch.cuda.current_stream(dev).cuda_stream)
+    if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, expected {dev}")
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield torch.cuda.current_stream(dev).cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def _raise(rc, name):
+    if rc != 0:
+        raise GdnError(rc, name)
 
 
 def _shapes(name, q, k, v, log_decay):
     """Checks q, k, v and log_decay; (rows, Hqk, Hv, Dk, Dv, dtype, device)."""
-    dev = q.device
+    dev, dt = q.device, q.dtype
     if dev.type != "cuda":
         raise ValueError(f"{name} runs on CUDA tensors only")
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError(f"{name}: q and v must have three dimensions")
     rows, Hqk, Dk = q.shape
-    Hv, Dv = v.shape[1], v.shape[2]
-    if q.dtype not in DTYPE:
-        raise ValueError(f"unsupported io dtype {q.dtype}")
-    _check(q, "q", (rows, Hqk, Dk), q.dtype, dev)
-    _check(k, "k", (rows, Hqk, Dk), q.dtype, dev)
-    _check(v, "v", (rows, Hv, Dv), q.dtype, dev)
-    _check(log_decay, "log_decay", (Hv,), F32, dev)
-    return rows, Hqk, Hv, Dk, Dv, q.dtype, dev
+    _, Hv, Dv = v.shape
+    if dt not in DTYPE:
+        raise ValueError(f"unsupported io dtype {dt}")
+    _need(q, "q", (rows, Hqk, Dk), dt, dev)
+    _need(k, "k", (rows, Hqk, Dk), dt, dev)
+    _need(v, "v", (rows, Hv, Dv), dt, dev)
+    _need(log_decay, "log_decay", (Hv,), F32, dev)
+    return rows, Hqk, Hv, Dk, Dv, dt, dev
 
 
 def _sequences(cu_seqlens, dev):
     if cu_seqlens is None:
         return 1
     N = cu_seqlens.shape[0] - 1
-    _check(cu_seqlens, "cu_seqlens", (N + 1,), I32, dev)
+    _need(cu_seqlens, "cu_seqlens", (N + 1,), I32, dev)
     return N
 
 
 def _flag(error_flag, dev):
     if error_flag is not None:
-        _check(error_flag, "error_flag", tuple(error_flag.shape), I32, dev)
+        _need(error_flag, "error_flag", tuple(error_flag.shape), I32, dev)
+
+
+def _slots(state_pool, slot_idx, reset, N, Hv, Dv, Dk, dev):
+    S = state_pool.shape[0]
+    _need(state_pool, "state_pool", (S, Hv, Dv, Dk), F32, dev)
+    _need(slot_idx, "slot_idx", (N,), I32, dev)
+    if reset is not None:
+        _need(reset, "reset", (N,), I32, dev)
+    return S
+
+
+def _output(t, name, shape, dtype, dev):
+    """`t`, checked, or a new tensor."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, shape, dtype, dev)
+    return t
 
 
 def _scratch(workspace, need, dev):
+    """(address, bytes, tensor) of the workspace, or of a new one."""
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous, on {dev}")
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if workspace is None:
+        return None, 0, None
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def gdn_linear_prefill_workspace_bytes(N, T, Hqk, Hv, Dk, Dv, dtype=torch.bfloat16):
@@ -89,25 +124,22 @@ def gdn_linear_prefill(q, k, v, log_decay, initial_state=None, cu_seqlens=None, 
     T, Hqk, Hv, Dk, Dv, dt, dev = _shapes("gdn_linear_prefill", q, k, v, log_decay)
     N = _sequences(cu_seqlens, dev)
     if initial_state is not None:
-        _check(initial_state, "initial_state", (N, Hv, Dv, Dk), F32, dev)
+        _need(initial_state, "initial_state", (N, Hv, Dv, Dk), F32, dev)
     _flag(error_flag, dev)
-    with _on(dev, stream) as st:
-        if o is None:
-            o = torch.empty((T, Hv, Dv), dtype=dt, device=dev)
-        _check(o, "o", (T, Hv, Dv), dt, dev)
-        if final_state is None and output_final_state:
-            final_state = torch.empty((N, Hv, Dv, Dk), dtype=F32, device=dev)
-        if final_state is not None:
-            _check(final_state, "final_state", (N, Hv, Dv, Dk), F32, dev)
-        workspace, ws_bytes = _scratch(
-            workspace, lib.gdn_linear_prefill_workspace_bytes(N, T, Hqk, Hv, Dk, Dv, DTYPE[dt]), dev)
-        rc = lib.gdn_linear_prefill(_ptr(q), _ptr(k), _ptr(v), DTYPE[dt], _ptr(log_decay), scale,
-                                    _ptr(initial_state), _ptr(cu_seqlens), N, T, Hqk, Hv, Dk, Dv,
-                                    _ptr(o), _ptr(final_state), _ptr(workspace), ws_bytes,
-                                    _ptr(error_flag), st)
-    if rc != 0:
-        raise GdnError(rc, "gdn_linear_prefill")
-    return o, final_state
+    sizes = (N, T, Hqk, Hv, Dk, Dv)
+
+    def call(st):
+        out = _output(o, "o", (T, Hv, Dv), dt, dev)
+        final = final_state
+        if final is not None or output_final_state:
+            final = _output(final, "final_state", (N, Hv, Dv, Dk), F32, dev)
+        ws, n, _keep = _scratch(workspace, lib.gdn_linear_prefill_workspace_bytes(*sizes, DTYPE[dt]), dev)
+        _raise(lib.gdn_linear_prefill(_at(q), _at(k), _at(v), DTYPE[dt], _at(log_decay), scale,
+                                      _at(initial_state), _at(cu_seqlens), *sizes, _at(out), _at(final), ws,
+                                      n, _at(error_flag), st), "gdn_linear_prefill")
+        return out, final
+
+    return _run(dev, stream, call)
 
 
 def gdn_linear_prefill_slots(q, k, v, log_decay, state_pool, slot_idx, reset=None, cu_seqlens=None, *,
@@ -117,25 +149,21 @@ def gdn_linear_prefill_slots(q, k, v, log_decay, state_pool, slot_idx, reset=Non
     is nonzero; slot_idx (distinct) and reset int32 [N].  Returns o."""
     lib = library()
     T, Hqk, Hv, Dk, Dv, dt, dev = _shapes("gdn_linear_prefill_slots", q, k, v, log_decay)
-    N, S = _sequences(cu_seqlens, dev), state_pool.shape[0]
-    _check(state_pool, "state_pool", (S, Hv, Dv, Dk), F32, dev)
-    _check(slot_idx, "slot_idx", (N,), I32, dev)
-    if reset is not None:
-        _check(reset, "reset", (N,), I32, dev)
+    N = _sequences(cu_seqlens, dev)
+    S = _slots(state_pool, slot_idx, reset, N, Hv, Dv, Dk, dev)
     _flag(error_flag, dev)
-    with _on(dev, stream) as st:
-        if o is None:
-            o = torch.empty((T, Hv, Dv), dtype=dt, device=dev)
-        _check(o, "o", (T, Hv, Dv), dt, dev)
-        workspace, ws_bytes = _scratch(
-            workspace, lib.gdn_linear_prefill_workspace_bytes(N, T, Hqk, Hv, Dk, Dv, DTYPE[dt]), dev)
-        rc = lib.gdn_linear_prefill_slots(_ptr(q), _ptr(k), _ptr(v), DTYPE[dt], _ptr(log_decay), scale,
-                                          _ptr(state_pool), S, _ptr(slot_idx), _ptr(reset),
-                                          _ptr(cu_seqlens), N, T, Hqk, Hv, Dk, Dv, _ptr(o),
-                                          _ptr(workspace), ws_bytes, _ptr(error_flag), st)
-    if rc != 0:
-        raise GdnError(rc, "gdn_linear_prefill_slots")
-    return o
+    sizes = (N, T, Hqk, Hv, Dk, Dv)
+
+    def call(st):
+        out = _output(o, "o", (T, Hv, Dv), dt, dev)
+        ws, n, _keep = _scratch(workspace, lib.gdn_linear_prefill_workspace_bytes(*sizes, DTYPE[dt]), dev)
+        _raise(lib.gdn_linear_prefill_slots(_at(q), _at(k), _at(v), DTYPE[dt], _at(log_decay), scale,
+                                            _at(state_pool), S, _at(slot_idx), _at(reset), _at(cu_seqlens),
+                                            *sizes, _at(out), ws, n, _at(error_flag), st),
+               "gdn_linear_prefill_slots")
+        return out
+
+    return _run(dev, stream, call)
 
 
 def gdn_linear_prefill_backward(do, q, k, v, log_decay, initial_state=None, cu_seqlens=None, *,
@@ -149,32 +177,29 @@ def gdn_linear_prefill_backward(do, q, k, v, log_decay, initial_state=None, cu_s
     lib = library()
     T, Hqk, Hv, Dk, Dv, dt, dev = _shapes("gdn_linear_prefill_backward", q, k, v, log_decay)
     N = _sequences(cu_seqlens, dev)
-    _check(do, "do", (T, Hv, Dv), dt, dev)
+    _need(do, "do", (T, Hv, Dv), dt, dev)
     for x, name in ((initial_state, "initial_state"), (dfinal_state, "dfinal_state")):
         if x is not None:
-            _check(x, name, (N, Hv, Dv, Dk), F32, dev)
+            _need(x, name, (N, Hv, Dv, Dk), F32, dev)
     _flag(error_flag, dev)
-    with _on(dev, stream) as st:
-        dq = torch.empty_like(q) if dq is None else dq
-        dk = torch.empty_like(k) if dk is None else dk
-        dv = torch.empty_like(v) if dv is None else dv
-        _check(dq, "dq", (T, Hqk, Dk), dt, dev)
-        _check(dk, "dk", (T, Hqk, Dk), dt, dev)
-        _check(dv, "dv", (T, Hv, Dv), dt, dev)
-        if dinitial_state is None and output_dinitial_state:
-            dinitial_state = torch.empty((N, Hv, Dv, Dk), dtype=F32, device=dev)
-        if dinitial_state is not None:
-            _check(dinitial_state, "dinitial_state", (N, Hv, Dv, Dk), F32, dev)
-        workspace, ws_bytes = _scratch(
-            workspace,
-            lib.gdn_linear_prefill_backward_workspace_bytes(N, T, Hqk, Hv, Dk, Dv, DTYPE[dt]), dev)
-        rc = lib.gdn_linear_prefill_backward(
-            _ptr(do), _ptr(q), _ptr(k), _ptr(v), DTYPE[dt], _ptr(log_decay), scale,
-            _ptr(initial_state), _ptr(dfinal_state), _ptr(cu_seqlens), N, T, Hqk, Hv, Dk, Dv, _ptr(dq),
-            _ptr(dk), _ptr(dv), _ptr(dinitial_state), _ptr(workspace), ws_bytes, _ptr(error_flag), st)
-    if rc != 0:
-        raise GdnError(rc, "gdn_linear_prefill_backward")
-    return dq, dk, dv, dinitial_state
+    sizes = (N, T, Hqk, Hv, Dk, Dv)
+
+    def call(st):
+        gq = _output(dq, "dq", (T, Hqk, Dk), dt, dev)
+        gk = _output(dk, "dk", (T, Hqk, Dk), dt, dev)
+        gv = _output(dv, "dv", (T, Hv, Dv), dt, dev)
+        gs = dinitial_state
+        if gs is not None or output_dinitial_state:
+            gs = _output(gs, "dinitial_state", (N, Hv, Dv, Dk), F32, dev)
+        ws, n, _keep = _scratch(
+            workspace, lib.gdn_linear_prefill_backward_workspace_bytes(*sizes, DTYPE[dt]), dev)
+        _raise(lib.gdn_linear_prefill_backward(_at(do), _at(q), _at(k), _at(v), DTYPE[dt], _at(log_decay),
+                                               scale, _at(initial_state), _at(dfinal_state), _at(cu_seqlens),
+                                               *sizes, _at(gq), _at(gk), _at(gv), _at(gs), ws, n,
+                                               _at(error_flag), st), "gdn_linear_prefill_backward")
+        return gq, gk, gv, gs
+
+    return _run(dev, stream, call)
 
 
 def gdn_linear_decode_step(q, k, v, log_decay, state, *, scale=1.0, o=None, error_flag=None,
@@ -183,17 +208,17 @@ def gdn_linear_decode_step(q, k, v, log_decay, state, *, scale=1.0, o=None, erro
     [N,Hqk,Dk], v [N,Hv,Dv] (bf16 or fp32), log_decay [Hv].  Returns o [N,Hv,Dv]."""
     lib = library()
     N, Hqk, Hv, Dk, Dv, dt, dev = _shapes("gdn_linear_decode_step", q, k, v, log_decay)
-    _check(state, "state", (N, Hv, Dv, Dk), F32, dev)
+    _need(state, "state", (N, Hv, Dv, Dk), F32, dev)
     _flag(error_flag, dev)
-    with _on(dev, stream) as st:
-        if o is None:
-            o = torch.empty((N, Hv, Dv), dtype=dt, device=dev)
-        _check(o, "o", (N, Hv, Dv), dt, dev)
-        rc = lib.gdn_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), DTYPE[dt], _ptr(log_decay), scale,
-                                        _ptr(state), N, Hqk, Hv, Dk, Dv, _ptr(o), _ptr(error_flag), st)
-    if rc != 0:
-        raise GdnError(rc, "gdn_linear_decode_step")
-    return o
+
+    def call(st):
+        out = _output(o, "o", (N, Hv, Dv), dt, dev)
+        _raise(lib.gdn_linear_decode_step(_at(q), _at(k), _at(v), DTYPE[dt], _at(log_decay), scale,
+                                          _at(state), N, Hqk, Hv, Dk, Dv, _at(out), _at(error_flag), st),
+               "gdn_linear_decode_step")
+        return out
+
+    return _run(dev, stream, call)
 
 
 def gdn_linear_decode_step_slots(q, k, v, log_decay, state_pool, slot_idx, reset=None, *, scale=1.0,
@@ -203,19 +228,15 @@ def gdn_linear_decode_step_slots(q, k, v, log_decay, state_pool, slot_idx, reset
     is nonzero; slot_idx (distinct) and reset int32 [N].  Returns o."""
     lib = library()
     N, Hqk, Hv, Dk, Dv, dt, dev = _shapes("gdn_linear_decode_step_slots", q, k, v, log_decay)
-    S = state_pool.shape[0]
-    _check(state_pool, "state_pool", (S, Hv, Dv, Dk), F32, dev)
-    _check(slot_idx, "slot_idx", (N,), I32, dev)
-    if reset is not None:
-        _check(reset, "reset", (N,), I32, dev)
+    S = _slots(state_pool, slot_idx, reset, N, Hv, Dv, Dk, dev)
     _flag(error_flag, dev)
-    with _on(dev, stream) as st:
-        if o is None:
-            o = torch.empty((N, Hv, Dv), dtype=dt, device=dev)
-        _check(o, "o", (N, Hv, Dv), dt, dev)
-        rc = lib.gdn_linear_decode_step_slots(_ptr(q), _ptr(k), _ptr(v), DTYPE[dt], _ptr(log_decay),
-                                              scale, _ptr(state_pool), S, _ptr(slot_idx), _ptr(reset),
-                                              N, Hqk, Hv, Dk, Dv, _ptr(o), _ptr(error_flag), st)
-    if rc != 0:
-        raise GdnError(rc, "gdn_linear_decode_step_slots")
-    return o
+
+    def call(st):
+        out = _output(o, "o", (N, Hv, Dv), dt, dev)
+        _raise(lib.gdn_linear_decode_step_slots(_at(q), _at(k), _at(v), DTYPE[dt], _at(log_decay), scale,
+                                                _at(state_pool), S, _at(slot_idx), _at(reset), N, Hqk, Hv,
+                                                Dk, Dv, _at(out), _at(error_flag), st),
+               "gdn_linear_decode_step_slots")
+        return out
+
+    return _run(dev, stream, call)

@@ -7,8 +7,8 @@ import ctypes
 
 import torch
 
-from . import DTYPE, GdnError, _check, _ptr, library
-from .linear import F32, I32, _on, _scratch
+from . import DTYPE, library
+from .linear import F32, I32, _at, _need, _output, _raise, _run, _scratch
 
 
 def _rows(x, name, T, D, dtype, dev):
@@ -20,9 +20,10 @@ def _rows(x, name, T, D, dtype, dev):
     if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D:
         raise ValueError(f"{name} has shape {tuple(x.shape)}, expected ({T}, heads, {D})")
     H = x.shape[1]
-    if x.numel() and (x.stride(2) != 1 or (H > 1 and x.stride(1) != D)):
+    step, head, one = x.stride()
+    if x.numel() and (one != 1 or (H > 1 and head != D)):
         raise ValueError(f"{name} must be contiguous within a token")
-    return H, x.stride(0) if T > 1 else H * D
+    return H, step if T > 1 else H * D
 
 
 def _setup(name, xq, xk, positions, inv_freq, wq, wk, sections):
@@ -36,18 +37,19 @@ def _setup(name, xq, xk, positions, inv_freq, wq, wk, sections):
     T, _, D = xq.shape
     Hq, sq = _rows(xq, "xq", T, D, dt, dev)
     Hk, sk = _rows(xk, "xk", T, D, dt, dev) if xk is not None else (0, 0)
-    for w, what in ((wq, "wq"), (wk, "wk")):
-        if w is not None:
-            _check(w, what, (D,), F32, dev)
+    if wq is not None:
+        _need(wq, "wq", (D,), F32, dev)
+    if wk is not None:
+        _need(wk, "wk", (D,), F32, dev)
     rot = axes = 0
     sec = None
     if (inv_freq is None) != (positions is None):
         raise ValueError("positions and inv_freq come together")
     if inv_freq is not None:
         rot = 2 * inv_freq.shape[0]
-        _check(inv_freq, "inv_freq", (rot // 2,), F32, dev)
+        _need(inv_freq, "inv_freq", (rot // 2,), F32, dev)
         axes = positions.shape[0] if positions.dim() == 2 else 1
-        _check(positions, "positions", (axes, T) if positions.dim() == 2 else (T,), I32, dev)
+        _need(positions, "positions", (axes, T) if positions.dim() == 2 else (T,), I32, dev)
         if sections is not None:
             if len(sections) != axes:
                 raise ValueError(f"{len(sections)} sections for {axes} position axes")
@@ -68,20 +70,16 @@ def gdn_qk_norm_rope(xq, xk=None, positions=None, inv_freq=None, *, wq=None, wk=
     lib = library()
     dev, dt, T, Hq, Hk, D, sq, sk, rot, axes, sec = _setup("gdn_qk_norm_rope", xq, xk, positions,
                                                            inv_freq, wq, wk, sections)
-    with _on(dev, stream) as st:
-        if q is None:
-            q = torch.empty((T, Hq, D), dtype=dt, device=dev)
-        _check(q, "q", (T, Hq, D), dt, dev)
-        if xk is not None:
-            if k is None:
-                k = torch.empty((T, Hk, D), dtype=dt, device=dev)
-            _check(k, "k", (T, Hk, D), dt, dev)
-        rc = lib.gdn_qk_norm_rope(_ptr(xq), _ptr(xk), DTYPE[dt], sq, sk, _ptr(wq), _ptr(wk), eps,
-                                  _ptr(positions), axes, sec, _ptr(inv_freq), rot, int(interleaved), T,
-                                  Hq, Hk, D, _ptr(q), _ptr(k), st)
-    if rc != 0:
-        raise GdnError(rc, "gdn_qk_norm_rope")
-    return q, k
+
+    def call(st):
+        zq = _output(q, "q", (T, Hq, D), dt, dev)
+        zk = None if xk is None else _output(k, "k", (T, Hk, D), dt, dev)
+        _raise(lib.gdn_qk_norm_rope(_at(xq), _at(xk), DTYPE[dt], sq, sk, _at(wq), _at(wk), eps,
+                                    _at(positions), axes, sec, _at(inv_freq), rot, int(interleaved), T, Hq,
+                                    Hk, D, _at(zq), _at(zk), st), "gdn_qk_norm_rope")
+        return zq, zk
+
+    return _run(dev, stream, call)
 
 
 def gdn_qk_norm_rope_backward(dq, dk, xq, xk=None, positions=None, inv_freq=None, *, wq=None, wk=None,
@@ -95,34 +93,31 @@ def gdn_qk_norm_rope_backward(dq, dk, xq, xk=None, positions=None, inv_freq=None
     lib = library()
     dev, dt, T, Hq, Hk, D, sq, sk, rot, axes, sec = _setup("gdn_qk_norm_rope_backward", xq, xk,
                                                            positions, inv_freq, wq, wk, sections)
-    _check(dq, "dq", (T, Hq, D), dt, dev)
+    _need(dq, "dq", (T, Hq, D), dt, dev)
     if xk is not None:
-        _check(dk, "dk", (T, Hk, D), dt, dev)
-    with _on(dev, stream) as st:
-        if dxq is None:
-            dxq = torch.empty((T, Hq, D), dtype=dt, device=dev)
-        h, dsq = _rows(dxq, "dxq", T, D, dt, dev)
+        _need(dk, "dk", (T, Hk, D), dt, dev)
+
+    def call(st):
+        gq = torch.empty((T, Hq, D), dtype=dt, device=dev) if dxq is None else dxq
+        h, dsq = _rows(gq, "dxq", T, D, dt, dev)
         if h != Hq:
             raise ValueError(f"dxq has {h} heads, expected {Hq}")
-        dsk = 0
+        gk, dsk = None, 0
         if xk is not None:
-            if dxk is None:
-                dxk = torch.empty((T, Hk, D), dtype=dt, device=dev)
-            h, dsk = _rows(dxk, "dxk", T, D, dt, dev)
+            gk = torch.empty((T, Hk, D), dtype=dt, device=dev) if dxk is None else dxk
+            h, dsk = _rows(gk, "dxk", T, D, dt, dev)
             if h != Hk:
                 raise ValueError(f"dxk has {h} heads, expected {Hk}")
         dwq = dwk = None
         if output_dweights:
             dwq = torch.empty(D, dtype=F32, device=dev)
-            if xk is not None:
-                dwk = torch.empty(D, dtype=F32, device=dev)
-        workspace, ws_bytes = _scratch(
+            dwk = None if xk is None else torch.empty(D, dtype=F32, device=dev)
+        ws, n, _keep = _scratch(
             workspace, lib.gdn_qk_norm_rope_backward_workspace_bytes(D) if output_dweights else 0, dev)
-        rc = lib.gdn_qk_norm_rope_backward(
-            _ptr(dq), _ptr(dk) if xk is not None else None, _ptr(xq), _ptr(xk), DTYPE[dt], sq, sk,
-            _ptr(wq), _ptr(wk), eps, _ptr(positions), axes, sec, _ptr(inv_freq), rot, int(interleaved),
-            T, Hq, Hk, D, _ptr(dxq), _ptr(dxk), dsq, dsk, _ptr(dwq), _ptr(dwk), _ptr(workspace),
-            ws_bytes, st)
-    if rc != 0:
-        raise GdnError(rc, "gdn_qk_norm_rope_backward")
-    return dxq, dxk, dwq, dwk
+        _raise(lib.gdn_qk_norm_rope_backward(
+            _at(dq), None if xk is None else _at(dk), _at(xq), _at(xk), DTYPE[dt], sq, sk, _at(wq), _at(wk),
+            eps, _at(positions), axes, sec, _at(inv_freq), rot, int(interleaved), T, Hq, Hk, D, _at(gq),
+            _at(gk), dsq, dsk, _at(dwq), _at(dwk), ws, n, st), "gdn_qk_norm_rope_backward")
+        return gq, gk, dwq, dwk
+
+    return _run(dev, stream, call)
