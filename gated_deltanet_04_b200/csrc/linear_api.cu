@@ -59,8 +59,13 @@ size_t seg_bytes(const Call &c, int64_t seg_len) {
     return seg_len ? al256((size_t)gdn::linear::slots_of(c.T, c.N, seg_len) * c.Hv * c.Dk * c.Dv * 4) : 0;
 }
 
-// The tensor-core kernels serve 128-wide bf16 heads.
-bool tensor_cores(const Call &c) { return c.dt == GDN_DTYPE_BF16 && c.Dk == 128 && c.Dv == 128 && c.T > 0; }
+// The tensor-core kernels serve 128-wide bf16 heads, from 16 tokens a sequence on
+// average: below that a token at a time is faster than 128-token chunks.  (48 heads:
+// 64 sequences of 16 tokens 326 us a token at a time and 318 on tensor cores, 4
+// sequences of 3 on average 11 and 32.)
+bool tensor_cores(const Call &c) {
+    return c.dt == GDN_DTYPE_BF16 && c.Dk == 128 && c.Dv == 128 && c.T > (int64_t)16 * c.N;
+}
 
 size_t prefill_bytes(const Call &c) {
     if (check(c) != GDN_OK || check_size(c) != GDN_OK || c.T == 0) return 0;

@@ -35,11 +35,6 @@ __device__ __forceinline__ float4 load4(const void *p, int64_t idx, gdn_dtype dt
     return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + idx);
 }
 
-// M[i][d] of an entering state stored plain or transposed.
-__device__ __forceinline__ float m0_at(const Pass &p, const float *base, int i, int d) {
-    return p.m0_transposed ? base[(int64_t)d * p.Dc + i] : base[(int64_t)i * p.Da + d];
-}
-
 template <int DA, bool kOut, bool kRev>
 __global__ void __launch_bounds__(kThreads)
     gdn_linear_recurrent_kernel(Pass p, int row_blocks) {
@@ -71,18 +66,24 @@ __global__ void __launch_bounds__(kThreads)
 
     // column m*4*LPR + 4*l + e of row rows[r]
     float M[RPT][16];
-    const bool from_m0 = kOut && !p.seg && p.m0 && st >= 0 && !state_fresh(p.map, sp.n);
+    const bool from_seg = kOut && p.seg && sp.count > 1;
+    const bool from_m0 = kOut && !from_seg && p.m0 && st >= 0 && !state_fresh(p.map, sp.n);
+    const float *src = from_seg ? p.seg + seg_off : from_m0 ? p.m0 + st_off : nullptr;
+    const bool across = from_m0 && p.m0_transposed;  // M[i][d] is at [d][i]
 #pragma unroll
     for (int r = 0; r < RPT; ++r)
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            const int i = row0 + rows[r], d = (x >> 2) * 4 * LPR + 4 * l + (x & 3);
-            float m = 0.f;
-            if (i < p.Dc) {
-                if (kOut && p.seg) m = p.seg[seg_off + (int64_t)i * DA + d];
-                else if (from_m0) m = m0_at(p, p.m0 + st_off, i, d);
+        for (int m = 0; m < 4; ++m) {
+            const int i = row0 + rows[r], d = m * 4 * LPR + 4 * l;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (src && i < p.Dc) {
+                if (across)
+                    v = make_float4(src[(int64_t)d * p.Dc + i], src[(int64_t)(d + 1) * p.Dc + i],
+                                    src[(int64_t)(d + 2) * p.Dc + i], src[(int64_t)(d + 3) * p.Dc + i]);
+                else
+                    v = *reinterpret_cast<const float4 *>(src + (int64_t)i * DA + d);
             }
-            M[r][x] = m;
+            M[r][4 * m] = v.x; M[r][4 * m + 1] = v.y; M[r][4 * m + 2] = v.z; M[r][4 * m + 3] = v.w;
         }
     const Decay decay(p.log_decay[h]);
     const int64_t len = sp.t1 - sp.t0;
@@ -139,40 +140,59 @@ __global__ void __launch_bounds__(kThreads)
         if (pos + kTokBlock < len) fetch(pos + kTokBlock);
         auto compute = [&](auto slow) {  // a uniform choice, made once per block of tokens
             constexpr bool kSlow = decltype(slow)::value;
-            for (int tt = 0; tt < nt; ++tt) {
-                float cv[RPT], acc[RPT];
-    #pragma unroll
-                for (int r = 0; r < RPT; ++r) {
-                    cv[r] = cs[tt][rows[r]];
-                    acc[r] = 0.f;
-                }
-    #pragma unroll
+            // one token: the read-outs' partial sums of this lane's columns
+            auto token_step = [&](int tt, float (&acc)[RPT]) {
+                float cv[RPT], part[RPT][4];
+#pragma unroll
+                for (int r = 0; r < RPT; ++r) cv[r] = cs[tt][rows[r]];
+#pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const float4 b4 = *reinterpret_cast<const float4 *>(&bs[tt][m * 4 * LPR + 4 * l]);
                     float4 a4;
                     if (kOut) a4 = *reinterpret_cast<const float4 *>(&as_[tt][m * 4 * LPR + 4 * l]);
                     const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
                     const float av[4] = {a4.x, a4.y, a4.z, a4.w};
-    #pragma unroll
-                    for (int r = 0; r < RPT; ++r)
-    #pragma unroll
+#pragma unroll
+                    for (int r = 0; r < RPT; ++r) {
+                        part[r][m] = 0.f;
+#pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float &x = M[r][4 * m + e];
                             if (!kRev) x = decay.times<kSlow>(x);
                             x = fmaf(cv[r], bv[e], x);
-                            if (kOut) acc[r] = fmaf(x, av[e], acc[r]);
+                            if (kOut) part[r][m] = fmaf(x, av[e], part[r][m]);
                             if (kRev) x = decay.times<kSlow>(x);
                         }
-                }
-                if (kOut) {
-    #pragma unroll
-                    for (int r = 0; r < RPT; ++r) {
-    #pragma unroll
-                        for (int off = LPR / 2; off > 0; off >>= 1)
-                            acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], off);
-                        if (l == 0) os[tt][rows[r]] = acc[r] * p.out_scale;
                     }
                 }
+#pragma unroll
+                for (int r = 0; r < RPT; ++r) acc[r] = (part[r][0] + part[r][1]) + (part[r][2] + part[r][3]);
+            };
+            // sums over the row's lanes, staged by the first of them
+            auto finish = [&](int tt, float (&acc)[RPT]) {
+#pragma unroll
+                for (int r = 0; r < RPT; ++r) {
+#pragma unroll
+                    for (int off = LPR / 2; off > 0; off >>= 1)
+                        acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], off);
+                    if (l == 0) os[tt][rows[r]] = acc[r] * p.out_scale;
+                }
+            };
+            // four tokens at a time: their sums' latencies overlap
+            int tt = 0;
+            for (; tt + 4 <= nt; tt += 4) {
+                float acc[4][RPT];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) token_step(tt + i, acc[i]);
+                if (kOut) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) finish(tt + i, acc[i]);
+                }
+            }
+            for (; tt < nt; ++tt) {
+                float acc[RPT];
+                token_step(tt, acc);
+                if (kOut) finish(tt, acc);
             }
         };
         if (decay.slow) compute(std::true_type{});
@@ -211,6 +231,7 @@ __global__ void gdn_linear_scan_kernel(Pass p) {
     int64_t t0, t1;
     if (!seq_range(p.cu, n, p.N, p.T, p.err, t0, t1)) return;
     const int64_t count = t1 > t0 ? (t1 - t0 + p.seg_len - 1) / p.seg_len : 1;
+    if (count == 1) return;  // the pass itself starts from the entering state
     const int64_t base = slot_base(p.cu, n, p.seg_len);
     const float g = p.log_decay[h];
     float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -319,7 +340,8 @@ cudaError_t launch_scan(const Pass &p, cudaStream_t s) {
 }
 
 // Enough segments for about eight of the 128-thread CTAs on each of 148 SMs,
-// none shorter than 256 tokens.
+// none shorter than 64 tokens (a token is 0.17 us of latency in a pass; the two
+// other launches and a state's traffic cost about as much as 64 of them).
 int64_t recurrent_seg_len(int32_t N, int64_t T, int32_t H, int32_t Da, int32_t Dc) {
     const int rows = Da == 16 ? 128 : 2 * kThreads / (Da / 16);
     const int64_t ctas = (int64_t)N * H * ((Dc + rows - 1) / rows);
@@ -327,7 +349,7 @@ int64_t recurrent_seg_len(int32_t N, int64_t T, int32_t H, int32_t Da, int32_t D
     const int64_t want = (148 * 8 + ctas - 1) / ctas;
     if (want <= 1) return 0;
     int64_t len = (T + want - 1) / want;
-    len = len < 256 ? 256 : (len + kTokBlock - 1) / kTokBlock * kTokBlock;
+    len = len < 64 ? 64 : (len + kTokBlock - 1) / kTokBlock * kTokBlock;
     return len < T ? len : 0;
 }
 

@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         const float *src = nullptr;
-        if (kDump && p.seg) src = p.seg + (slot * p.H + h) * (int64_t)(kD * kD) + at;
+        if (kDump && p.seg && sp.count > 1) src = p.seg + (slot * p.H + h) * (int64_t)(kD * kD) + at;
         else if (kDump && p.m0 && st >= 0 && !state_fresh(p.map, sp.n))
             src = p.m0 + (st * p.H + h) * (int64_t)(kD * kD) + at;
 #pragma unroll
@@ -444,19 +444,19 @@ int device_sms() {
     return sms;
 }
 
-// Segments when the (sequence, head) units alone would leave SMs idle: as many
-// as let whole waves of 148 CTAs share the chunks, up to four waves for long
-// sequences (a shorter last wave), none under 4 chunks.
+// Segments, when one sequence could keep a CTA busy for much longer than an even
+// share of all chunks would: the segment sums walk the chunks a second time, so
+// it has to be beyond 2.5 shares (and some launches: 8 chunks' time).  Measured
+// with 48 heads: 4,096 tokens of one sequence 72 us with and 77 without, 65,536
+// tokens 840 and 1,230.  As many segments as let whole waves of 148 CTAs share
+// the chunks, up to four for long sequences (a shorter last wave).
 int64_t state_seg_chunks(int32_t N, int64_t T, int32_t H) {
-    const int64_t chunks = T / kC + 1, units = (int64_t)N * H;
-    if (units <= 0 || T <= 0) return 0;
-    int64_t waves = chunks * H / (148 * 16);
+    const int64_t longest = T / kC + 1, all = (T / kC + N) * H, share = all / 148;
+    if (N <= 0 || T <= 0 || longest <= 3 * share + 2) return 0;
+    int64_t waves = all / (148 * 16);
     waves = waves < 1 ? 1 : waves > 4 ? 4 : waves;
-    const int64_t want = 148 * waves / H;  // segments, were all of one sequence's length
-    if (want <= 1) return 0;
-    int64_t len = (chunks + want - 1) / want;
-    len = len < 4 ? 4 : len;
-    return len < chunks ? len : 0;
+    const int64_t len = (all + 148 * waves - 1) / (148 * waves);
+    return len < 4 ? 4 : len;
 }
 
 size_t state_seg_bytes(int32_t N, int64_t T, int32_t H) {
