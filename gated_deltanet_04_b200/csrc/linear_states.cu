@@ -51,7 +51,9 @@ struct Columns {
 static_assert(Columns<2>::parts(2) <= 512 && Columns<3>::parts(2) <= 512, "tensor memory");
 
 struct Misc {
-    alignas(16) uint32_t weight[2][3][kC / 2];  // of token pairs, in parts: a whole chunk's, the partial chunk's
+    // of token pairs, a whole chunk's and the partial chunk's: as two bf16 parts, and in fp32
+    alignas(16) uint32_t weight[2][2][kC / 2];
+    alignas(16) float2 weight32[2][kC / 2];
     uint64_t raw_full[kRing], raw_empty[kRing], part_full[2], part_empty[2], sum_full[2], sum_empty[2], drain;
     uint32_t tmem;
     volatile int32_t abort;
@@ -89,7 +91,7 @@ __device__ void produce(const CUtensorMap &tm_y, const Walk &w, int hy, uint8_t 
     }
 }
 
-// Packed bf16 pairs: fused multiply-add, product, difference, one rounding each.
+// Packed bf16 pairs: fused multiply-add, product, one rounding each.
 __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -98,24 +100,21 @@ __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     return fma2(a, b, 0x80008000u);  // - 0: keeps the sign of a zero product
 }
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) { return fma2(b, 0xbf80bf80u, a); }  // a - b
 
-// The weights of a chunk of L tokens (0 past its end) as bf16 parts hi + mid + lo
-// (24 bits) of pairs of tokens; thread i < 64 has pair i.
-__device__ __forceinline__ void make_weights(uint32_t (*dst)[kC / 2], int i, int L, bool reverse, float l2,
+// The weights of a chunk of L tokens (0 past its end), of pairs of tokens; thread i <
+// 64 has pair i.
+__device__ __forceinline__ void make_weights(Misc *ms, int which, int i, int L, bool reverse, float l2,
                                              float x_scale) {
     auto weight = [&](int j) {
         if (j >= L) return 0.f;
         return reverse ? x_scale * exp2f(l2 * (float)(j + 1)) : exp2f(l2 * (float)(L - 1 - j));
     };
-    float2 f = make_float2(weight(2 * i), weight(2 * i + 1));
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        const uint32_t part = pack_bf16(f);
-        dst[k][i] = part;
-        const float2 g = unpack_bf16(part);
-        f = make_float2(f.x - g.x, f.y - g.y);
-    }
+    const float2 f = make_float2(weight(2 * i), weight(2 * i + 1));
+    ms->weight32[which][i] = f;
+    const uint32_t hi = pack_bf16(f);
+    const float2 g = unpack_bf16(hi);
+    ms->weight[which][0][i] = hi;
+    ms->weight[which][1][i] = pack_bf16(f.x - g.x, f.y - g.y);
 }
 
 __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]) {
@@ -124,13 +123,14 @@ __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]
                  : "memory");
 }
 
-// Every second stage (group 0 or 1): x^T w = hi + mid + lo into tensor memory, a
-// thread per row (column of x) and 32 of the tokens, in packed bf16 arithmetic
-// (fused multiply-adds, one rounding each): hi = x wh rounded; x wh - hi is exact
-// (16 bits less the upper 8), so mid = x wm + (x wh - hi) is rounded once, and lo
-// takes what mid's rounding left and x wl.  A pair of lanes loads its two columns
-// of two tokens, a token each, and swaps halves.  x: this lane pair's columns of
-// token 0, `stride` elements from token to token.
+// Every second stage (group 0 or 1): x^T w into tensor memory, a thread per row
+// (column of x) and 32 of the tokens.  Two parts, in packed bf16 arithmetic (fused
+// multiply-adds, one rounding each): hi = x wh rounded; x wh - hi is exact (16 bits
+// less the upper 8), so mid = x wm + (x wh - hi) is rounded once, 2^-17 of the
+// product.  Three parts in fp32: each takes what the ones before left of x w, whose
+// own rounding is fp32's.  A pair of lanes loads its two columns of two tokens, a
+// token each, and swaps halves.  x: this lane pair's columns of token 0, `stride`
+// elements from token to token.
 template <int kParts>
 __device__ void convert(const Walk &w, const __nv_bfloat16 *x, int64_t stride, uint8_t *sm, Misc *ms, uint32_t tlane,
                         int group, int half, int tid, int32_t *err) {
@@ -170,6 +170,7 @@ __device__ void convert(const Walk &w, const __nv_bfloat16 *x, int64_t stride, u
     for (uint32_t r = group; a.it < w.nch; r += 2) {
         const int L = w.length(a.it), left = L - a.s * kRows;
         const uint32_t(*wt)[kC / 2] = ms->weight[L < kC];
+        const float2 *w32 = ms->weight32[L < kC];
         const int at = a.s * (kRows / 2) + 16 * half;
 #pragma unroll
         for (int q = 0; q < 16; ++q)  // this lane's column, two tokens
@@ -177,23 +178,33 @@ __device__ void convert(const Walk &w, const __nv_bfloat16 *x, int64_t stride, u
 #pragma unroll
         for (int q0 = 0; q0 < 16; q0 += 8) {
             uint32_t hi[8], mid[8], lo[8];
+            if constexpr (kParts == 2) {
 #pragma unroll
-            for (int q = 0; q < 8; q += 4) {
-                const uint4 h4 = *reinterpret_cast<const uint4 *>(&wt[0][at + q0 + q]);
-                const uint4 m4 = *reinterpret_cast<const uint4 *>(&wt[1][at + q0 + q]);
-                const uint32_t wh[4] = {h4.x, h4.y, h4.z, h4.w}, wm[4] = {m4.x, m4.y, m4.z, m4.w};
-                uint32_t wl[4] = {0u, 0u, 0u, 0u};
-                if (kParts == 3) {
-                    const uint4 l4 = *reinterpret_cast<const uint4 *>(&wt[2][at + q0 + q]);
-                    wl[0] = l4.x; wl[1] = l4.y; wl[2] = l4.z; wl[3] = l4.w;
+                for (int q = 0; q < 8; q += 4) {
+                    const uint4 h4 = *reinterpret_cast<const uint4 *>(&wt[0][at + q0 + q]);
+                    const uint4 m4 = *reinterpret_cast<const uint4 *>(&wt[1][at + q0 + q]);
+                    const uint32_t wh[4] = {h4.x, h4.y, h4.z, h4.w}, wm[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t v = next[q0 + q + e];
+                        hi[q + e] = mul2(v, wh[e]);
+                        mid[q + e] = fma2(v, wm[e], fma2(v, wh[e], hi[q + e] ^ 0x80008000u));
+                    }
                 }
+            } else {
+                const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t v = next[q0 + q + e], h = mul2(v, wh[e]);
-                    const uint32_t rest = fma2(v, wh[e], h ^ 0x80008000u), m = fma2(v, wm[e], rest);
-                    hi[q + e] = h;
-                    mid[q + e] = m;
-                    if (kParts == 3) lo[q + e] = fma2(v, wl[e], fma2(v, wm[e], sub2(rest, m)));
+                for (int q = 0; q < 8; q += 2) {
+                    const float4 f4 = *reinterpret_cast<const float4 *>(&w32[at + q0 + q]);
+                    const float2 f[2] = {make_float2(f4.x, f4.y), make_float2(f4.z, f4.w)};
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float2 left2 = fmul2(unpack_bf16(next[q0 + q + e]), f[e]);
+                        hi[q + e] = pack_bf16(left2);
+                        left2 = ffma2(unpack_bf16(hi[q + e]), minus, left2);
+                        mid[q + e] = pack_bf16(left2);
+                        lo[q + e] = pack_bf16(ffma2(unpack_bf16(mid[q + e]), minus, left2));
+                    }
                 }
             }
             // as late as can be: the MMAs of the other group's stage cover what follows
@@ -303,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbarrier_init();
     }
     if (tid < kC / 2) {
-        make_weights(ms->weight[0], tid, kC, w.reverse, l2, p.x_scale);
-        make_weights(ms->weight[1], tid, w.len % kC, w.reverse, l2, p.x_scale);
+        make_weights(ms, 0, tid, kC, w.reverse, l2, p.x_scale);
+        make_weights(ms, 1, tid, w.len % kC, w.reverse, l2, p.x_scale);
     }
     if (warp == 0) {
         tmem_alloc(&ms->tmem, 512);
