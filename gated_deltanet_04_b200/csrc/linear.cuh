@@ -73,24 +73,29 @@ struct Span {
 // same slot.  An empty sequence has one empty span, which carries its state.
 __device__ __forceinline__ bool find_span(const int32_t *cu, int32_t N, int64_t T, int64_t len,
                                           int64_t slot, int32_t *err, Span &sp) {
-    int64_t b, e;
-    // whatever the slots of a malformed cu_seqlens map to, each of its ranges
-    // is looked at by the CTAs of one slot
-    if (slot < N) seq_range(cu, (int)slot, N, T, err, b, e);
     int lo = 0, hi = N - 1;
     while (lo < hi) {  // the last n whose first slot is <= slot
         const int mid = (lo + hi + 1) >> 1;
         if (slot_base(cu, mid, len) <= slot) lo = mid;
         else hi = mid - 1;
     }
+    int64_t b, e;
     if (!seq_range(cu, lo, N, T, err, b, e)) return false;
     sp.n = lo;
-    sp.s = slot - slot_base(cu, lo, len);
+    sp.s = slot - (b / len + lo);
     sp.count = e > b ? (e - b + len - 1) / len : 1;
     if (sp.s < 0 || sp.s >= sp.count) return false;
     sp.t0 = b + sp.s * len;
     sp.t1 = sp.t0 + len < e ? sp.t0 + len : e;
     return true;
+}
+
+// Whatever the slots of a malformed cu_seqlens map to, each of its ranges is
+// looked at (and reported) by the CTAs of one slot, in a warp that is not first
+// to work: slots >= N.
+__device__ __forceinline__ void check_range(const int32_t *cu, int32_t N, int64_t T, int64_t slot, int32_t *err) {
+    int64_t b, e;
+    if (cu != nullptr && slot < N) seq_range(cu, (int)slot, N, T, err, b, e);
 }
 
 inline int64_t slots_of(int64_t T, int32_t N, int64_t len) { return T / len + N; }

@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kThreads)
     const int rb = blockIdx.x % row_blocks;
     const int h = (blockIdx.x / row_blocks) % p.H;
     const int64_t slot = blockIdx.x / (row_blocks * p.H);
+    if (tid == kThreads - 1) check_range(p.cu, p.N, p.T, slot, p.err);
     Span sp;
     if (!find_span(p.cu, p.N, p.T, p.seg ? p.seg_len : (p.T > 0 ? p.T : 1), slot, p.err, sp)) return;
     const bool last = kRev ? sp.s == 0 : sp.s == sp.count - 1;  // in the pass's order

@@ -12,15 +12,16 @@
 // come of it (a segment that does not end its sequence), hi + mid do.
 //
 // The parts of x^T (128 rows, 64 tokens a stage) are the MMAs' first operand in
-// tensor memory, one row per lane: the converting threads load x from global
-// memory with a lane per column, which transposes it on the way.  (With both
-// operands in shared memory the products alone took all of its bandwidth, and
-// the kernel 2.6 us a chunk.)
+// tensor memory, one row per lane: the converting threads read x from shared
+// memory with a lane per column, which transposes it on the way.
 //
-// Roles, on stages of 64 tokens: a producer warp loads y by TMA into a ring; two
-// groups of 8 warps take stages in turn, each writing x's parts into a buffer of
-// its own; an MMA warp sums a chunk's stages into an accumulator; 8 warps add it to
-// the state and store the image of the state that enters the next chunk.
+// Roles, on stages of 64 tokens: a producer warp loads x and y by TMA into a ring
+// of five; two groups of 8 warps take stages in turn, each writing x's parts into a
+// buffer of its own; an MMA warp sums a chunk's stages into an accumulator; 8
+// warps add it to the state and store the image of the state that enters the
+// next chunk.  (Tried: one set of warps doing all of it in turn, 3.3 us a chunk;
+// x's parts in shared memory, whose bandwidth the products then need whole, 2.6;
+// x from global memory to registers, a load's latency of 2,000 clocks a stage, 2.3.)
 // Bound: HBM (64 KB in, 32 KB image out per chunk and head, y shared by the
 // heads of a group through L2) against two or three products of 4.2 MFLOP.
 #include "linear_tc.cuh"
@@ -32,11 +33,12 @@ namespace {
 constexpr int kRows = 64;                    // tokens per stage
 constexpr uint32_t kHalf = kRows * 128;      // 64 rows x 64 columns
 constexpr uint32_t kPart = 2 * kHalf;        // 64 x 128 bf16
-constexpr int kRing = 8;                     // stages of y
+constexpr int kRing = 5;                     // stages of x and y
 constexpr int kStateWarps = 8, kConvWarps = 16, kGroup = 8;  // warps; warps per converting group
 constexpr int kStateThreads = kStateWarps * 32, kConvThreads = kConvWarps * 32;
 constexpr int kThreads = kStateThreads + kConvThreads + 64;
-constexpr uint32_t OFF_IMAGE = kRing * kPart;
+constexpr uint32_t kStage = 2 * kPart;       // x, y
+constexpr uint32_t OFF_IMAGE = kRing * kStage;
 constexpr uint32_t OFF_MISC = OFF_IMAGE + kTile;
 
 // Tensor memory columns: the state, the sum; then with two parts a second sum
@@ -70,7 +72,8 @@ struct Walk {
     __device__ __forceinline__ int length(int it) const { return min(len - chunk(it) * kC, kC); }
 };
 
-__device__ void produce(const CUtensorMap &tm_y, const Walk &w, int hy, uint8_t *sm, Misc *ms, int32_t *err) {
+__device__ void produce(const CUtensorMap &tm_x, const CUtensorMap &tm_y, const Walk &w, int h, int hy, uint8_t *sm,
+                        Misc *ms, int32_t *err) {
     uint32_t r = 0;  // stages so far
     for (int it = 0; it < w.nch; ++it) {
         const int L = w.length(it);
@@ -82,9 +85,11 @@ __device__ void produce(const CUtensorMap &tm_y, const Walk &w, int hy, uint8_t 
                     mbar_wait_bounded(&ms->raw_full[x % kRing], (x / kRing) & 1, kWaitLimit);
                 return;
             }
-            uint8_t *y = sm + b * kPart;
+            uint8_t *x = sm + b * kStage, *y = x + kPart;
             const int32_t t = (int32_t)w.t0 + w.chunk(it) * kC + j0;
-            mbar_arrive_expect_tx(&ms->raw_full[b], kPart);
+            mbar_arrive_expect_tx(&ms->raw_full[b], kStage);
+            tma_load_3d(x, &tm_x, &ms->raw_full[b], 0, h, t);
+            tma_load_3d(x + kHalf, &tm_x, &ms->raw_full[b], 64, h, t);
             tma_load_3d(y, &tm_y, &ms->raw_full[b], 0, hy, t);
             tma_load_3d(y + kHalf, &tm_y, &ms->raw_full[b], 64, hy, t);
         }
@@ -128,12 +133,11 @@ __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]
 // multiply-adds, one rounding each): hi = x wh rounded; x wh - hi is exact (16 bits
 // less the upper 8), so mid = x wm + (x wh - hi) is rounded once, 2^-17 of the
 // product.  Three parts in fp32: each takes what the ones before left of x w, whose
-// own rounding is fp32's.  A pair of lanes loads its two columns of two tokens, a
-// token each, and swaps halves.  x: this lane pair's columns of token 0, `stride`
-// elements from token to token.
+// own rounding is fp32's.  A pair of lanes reads its two columns of two tokens, a
+// token each, and swaps halves.
 template <int kParts>
-__device__ void convert(const Walk &w, const __nv_bfloat16 *x, int64_t stride, uint8_t *sm, Misc *ms, uint32_t tlane,
-                        int group, int half, int tid, int32_t *err) {
+__device__ void convert(const Walk &w, uint8_t *sm, Misc *ms, uint32_t tlane, int group, int half, int tid,
+                        int32_t *err) {
     struct At {  // stage s of chunk it
         int it, s;
     };
@@ -148,33 +152,32 @@ __device__ void convert(const Walk &w, const __nv_bfloat16 *x, int64_t stride, u
     };
     const int odd = tid & 1;
     const uint32_t swap = odd ? 0x3276u : 0x5410u;
-    uint32_t next[16];  // the group's next stage: tokens 2 q + odd, two columns
-    auto load = [&](const At &a) {
-        if (a.it >= w.nch) return;
-        const int j0 = a.s * kRows + 32 * half, left = w.length(a.it) - j0 - odd;
-        const __nv_bfloat16 *src = x + (w.t0 + w.chunk(a.it) * kC + j0 + odd) * stride;
-        const int64_t step = 2 * stride;
-        if (left >= 31) {
+    // tokens 32 half + 2 q + odd of a stage, this lane pair's columns: the swizzle repeats every 4 q
+    const int row = tid & 127, col = row & ~1;
+    uint32_t at_q[4];
 #pragma unroll
-            for (int q = 0; q < 16; ++q) next[q] = __ldg(reinterpret_cast<const uint32_t *>(src + q * step));
-        } else {
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-                next[q] = 2 * q < left ? __ldg(reinterpret_cast<const uint32_t *>(src + q * step)) : 0u;
-        }
-    };
+    for (int q = 0; q < 4; ++q) at_q[q] = (col >> 6) * kHalf + sw128(32 * half + 2 * q + odd, (col & 63) * 2);
     const uint32_t dst = tlane + Columns<kParts>::parts(group) + 16 * half;
     At a{0, 0};
     if (group == 1) a = w.length(0) > kRows ? At{0, 1} : At{1, 0};
-    load(a);
     for (uint32_t r = group; a.it < w.nch; r += 2) {
-        const int L = w.length(a.it), left = L - a.s * kRows;
+        const int L = w.length(a.it), left = L - a.s * kRows, b = r % kRing;
         const uint32_t(*wt)[kC / 2] = ms->weight[L < kC];
         const float2 *w32 = ms->weight32[L < kC];
         const int at = a.s * (kRows / 2) + 16 * half;
+        if (!role_wait(&ms->raw_full[b], (r / kRing) & 1, &ms->abort, err)) return;
+        const uint8_t *x = sm + b * kStage;
+        uint32_t in[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) in[q] = *reinterpret_cast<const uint32_t *>(x + at_q[q & 3] + (q >> 2) * 1024);
+        if (left < kRows) {  // a neighbour's rows
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                if (32 * half + 2 * q + odd >= left) in[q] = 0u;
+        }
 #pragma unroll
         for (int q = 0; q < 16; ++q)  // this lane's column, two tokens
-            next[q] = __byte_perm(next[q], __shfl_xor_sync(0xffffffffu, next[q], 1), swap);
+            in[q] = __byte_perm(in[q], __shfl_xor_sync(0xffffffffu, in[q], 1), swap);
 #pragma unroll
         for (int q0 = 0; q0 < 16; q0 += 8) {
             uint32_t hi[8], mid[8], lo[8];
@@ -186,7 +189,7 @@ __device__ void convert(const Walk &w, const __nv_bfloat16 *x, int64_t stride, u
                     const uint32_t wh[4] = {h4.x, h4.y, h4.z, h4.w}, wm[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint32_t v = next[q0 + q + e];
+                        const uint32_t v = in[q0 + q + e];
                         hi[q + e] = mul2(v, wh[e]);
                         mid[q + e] = fma2(v, wm[e], fma2(v, wh[e], hi[q + e] ^ 0x80008000u));
                     }
@@ -199,7 +202,7 @@ __device__ void convert(const Walk &w, const __nv_bfloat16 *x, int64_t stride, u
                     const float2 f[2] = {make_float2(f4.x, f4.y), make_float2(f4.z, f4.w)};
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float2 left2 = fmul2(unpack_bf16(next[q0 + q + e]), f[e]);
+                        float2 left2 = fmul2(unpack_bf16(in[q0 + q + e]), f[e]);
                         hi[q + e] = pack_bf16(left2);
                         left2 = ffma2(unpack_bf16(hi[q + e]), minus, left2);
                         mid[q + e] = pack_bf16(left2);
@@ -214,10 +217,9 @@ __device__ void convert(const Walk &w, const __nv_bfloat16 *x, int64_t stride, u
             if (kParts == 3) tmem_st8u(dst + 64 + q0, lo);
         }
         if (left < kRows) {  // y of the next sequence: 0 times its NaN would reach this sum
-            const int b = r % kRing;
-            if (!role_wait(&ms->raw_full[b], (r / kRing) & 1, &ms->abort, err)) return;
+            uint8_t *y = sm + b * kStage + kPart;
             for (int k = tid; k < (kRows - left) * 16; k += 32 * kGroup)
-                *reinterpret_cast<uint4 *>(sm + b * kPart + (k & 1) * kHalf + left * 128 + (k >> 1) * 16) =
+                *reinterpret_cast<uint4 *>(y + (k & 1) * kHalf + left * 128 + (k >> 1) * 16) =
                     make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
         }
@@ -225,7 +227,6 @@ __device__ void convert(const Walk &w, const __nv_bfloat16 *x, int64_t stride, u
         tc_fence_before_sync();
         warp_arrive(&ms->part_full[group]);
         a = advance(a);
-        load(a);
     }
 }
 
@@ -234,7 +235,7 @@ template <int kParts>
 __device__ void multiply(const Walk &w, uint32_t sbase, uint32_t tmem, Misc *ms, int32_t *err) {
     uint32_t r = 0, b = 0, lap = 0;  // stages so far; the ring's stage and lap
     constexpr int kSums = Columns<kParts>::kSums;
-    const uint64_t y0 = desc_m(sbase, kHalf);
+    const uint64_t y0 = desc_m(sbase + kPart, kHalf);
     bool ok = true;
     for (int it = 0; ok && it < w.nch; ++it) {
         const int L = w.length(it);
@@ -249,7 +250,7 @@ __device__ void multiply(const Walk &w, uint32_t sbase, uint32_t tmem, Misc *ms,
                        role_wait(&ms->part_full[buf], (r >> 1) & 1, &ms->abort, err)))
                 break;
             tc_fence_after_sync();
-            const uint64_t y = y0 + b * (kPart >> 4);
+            const uint64_t y = y0 + b * (kStage >> 4);
             const uint32_t x = tmem + Columns<kParts>::parts(buf);
 #pragma unroll
             for (int k = 0; k < kParts; ++k)
@@ -279,7 +280,8 @@ __device__ __forceinline__ void state_barrier() {
 // kDump: the pass proper (images, final state); otherwise the segments' sums.
 template <bool kDump>
 __global__ void __launch_bounds__(kThreads, 1)
-    gdn_linear_states_kernel(const __grid_constant__ CUtensorMap tm_y, StatePass p) {
+    gdn_linear_states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
+                             StatePass p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Misc *ms = reinterpret_cast<Misc *>(sm + OFF_MISC);
@@ -288,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = blockIdx.x % p.H;
     const int64_t slot = blockIdx.x / p.H;
     const int64_t seg_len = p.seg ? p.seg_chunks * kC : (p.T > 0 ? p.T : 1);
+    if (tid == kThreads - 1) check_range(p.cu, p.N, p.T, slot, p.err);
     Span sp;
     if (!find_span(p.cu, p.N, p.T, seg_len, slot, p.err, sp)) return;
     const bool last = p.reverse ? sp.s == 0 : sp.s == sp.count - 1;  // in the pass's order
@@ -331,12 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (cw < kConvWarps) {
             // warp % 4 is the quarter of the lanes a warp may write
             const int quad = warp & 3, row = quad * 32 + lane, half = (cw >> 2) & 1, group = cw / kGroup;
-            const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)h * kD + (row & ~1);
             const uint32_t tlane = tmem + ((uint32_t)(quad * 32) << 16);
-            if (w.nch > 0 && exact) convert<3>(w, x, (int64_t)p.H * kD, sm, ms, tlane, group, half, row + 128 * half, p.err);
-            else if (w.nch > 0) convert<2>(w, x, (int64_t)p.H * kD, sm, ms, tlane, group, half, row + 128 * half, p.err);
+            if (w.nch > 0 && exact) convert<3>(w, sm, ms, tlane, group, half, row + 128 * half, p.err);
+            else if (w.nch > 0) convert<2>(w, sm, ms, tlane, group, half, row + 128 * half, p.err);
         } else if (cw == kConvWarps) {
-            if (lane == 0) produce(tm_y, w, hy, sm, ms, p.err);
+            if (lane == 0) produce(tm_x, tm_y, w, h, hy, sm, ms, p.err);
         } else if (lane == 0) {
             if (exact) multiply<3>(w, smem_u32(sm), tmem, ms, p.err);
             else multiply<2>(w, smem_u32(sm), tmem, ms, p.err);
@@ -370,15 +372,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (kDump && p.m0 && st >= 0 && !state_fresh(p.map, sp.n))
             src = p.m0 + (st * p.H + h) * (int64_t)(kD * kD) + at;
 #pragma unroll
-        for (int c = 0; c < 64; c += 16) {
-            float v[16];
+        for (int c = 0; c < 64; c += 32) {  // a whole 128-byte line per thread at a time
+            float v[32];
 #pragma unroll
-            for (int x = 0; x < 16; x += 4) {
+            for (int x = 0; x < 32; x += 4) {
                 const float4 f = src ? *reinterpret_cast<const float4 *>(src + c + x) : make_float4(0.f, 0.f, 0.f, 0.f);
                 v[x] = f.x; v[x + 1] = f.y; v[x + 2] = f.z; v[x + 3] = f.w;
             }
-            tmem_st16(trow + TM_S + c, v);
-            if (kDump && w.nch > 0) draw(c, v);
+            tmem_st32(trow + TM_S + c, v);
+            if (kDump && w.nch > 0) {
+                draw(c, v);
+                draw(c + 16, v + 16);
+            }
         }
         tmem_wait_st();
         if (kDump && w.nch > 0) store_image(0);
@@ -403,14 +408,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld16(trow + TM_S + c, v);
                 tmem_ld16(trow + TM_SUM + 128 * sum + c, d);
                 tmem_wait_ld();
+                if (c == 48) {  // the sum has been read
+                    tc_fence_before_sync();
+                    warp_arrive(&ms->sum_empty[sum]);
+                }
 #pragma unroll
                 for (int x = 0; x < 16; ++x) v[x] = fmaf(dec, v[x], d[x]);
                 tmem_st16(trow + TM_S + c, v);
                 if (more) draw(c, v);
             }
             tmem_wait_st();
-            tc_fence_before_sync();
-            warp_arrive(&ms->sum_empty[sum]);
             if (more) store_image(it + 1);
         }
         float *dst = kDump ? (last && p.mT && st >= 0 ? p.mT + (st * p.H + h) * (int64_t)(kD * kD) : nullptr)
@@ -422,8 +429,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(trow + TM_S + c, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int x = 0; x < 32; x += 4)
-                    *reinterpret_cast<float4 *>(dst + at + c + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+                for (int x = 0; x < 32; x += 8) {
+                    uint32_t u[8];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) u[y] = __float_as_uint(v[x + y]);
+                    store_b256(dst + at + c + x, u);
+                }
             }
         }
         if (kDump && tid == 0) bulk_wait_all();
@@ -436,14 +447,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kDump>
-cudaError_t launch(const CUtensorMap &my, const StatePass &p, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &my, const StatePass &p, cudaStream_t s) {
     const int64_t len = p.seg ? p.seg_chunks * kC : (p.T > 0 ? p.T : 1);
     const int64_t blocks = slots_of(p.T, p.N, len) * p.H;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(gdn_linear_states_kernel<kDump>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    gdn_linear_states_kernel<kDump><<<(unsigned)blocks, kThreads, kSmem, s>>>(my, p);
+    gdn_linear_states_kernel<kDump><<<(unsigned)blocks, kThreads, kSmem, s>>>(mx, my, p);
     return cudaGetLastError();
 }
 
@@ -456,17 +467,14 @@ int device_sms() {
 }
 
 // Segments, when one sequence could keep a CTA busy for much longer than an even
-// share of all chunks would: the segment sums walk the chunks a second time, so
-// it has to be beyond 2.5 shares (and some launches: 8 chunks' time).  Measured
-// with 48 heads: 4,096 tokens of one sequence 72 us with and 77 without, 65,536
-// tokens 840 and 1,230.  As many segments as let whole waves of 148 CTAs share
-// the chunks, up to four for long sequences (a shorter last wave).
+// share of all chunks would (the segment sums walk the chunks a second time): as
+// long as the share, so that one wave of 148 CTAs has them all.  Measured with 48
+// heads and one sequence: 4,096 tokens 72 us with and 77 without, 65,536 tokens 550
+// and 800; segments for four waves 664.
 int64_t state_seg_chunks(int32_t N, int64_t T, int32_t H) {
     const int64_t longest = T / kC + 1, all = (T / kC + N) * H, share = all / 148;
     if (N <= 0 || T <= 0 || longest <= 3 * share + 2) return 0;
-    int64_t waves = all / (148 * 16);
-    waves = waves < 1 ? 1 : waves > 4 ? 4 : waves;
-    const int64_t len = (all + 148 * waves - 1) / (148 * waves);
+    const int64_t len = (all + 147) / 148;
     return len < 4 ? 4 : len;
 }
 
@@ -478,11 +486,12 @@ size_t state_seg_bytes(int32_t N, int64_t T, int32_t H) {
 size_t state_dump_bytes(int32_t N, int64_t T, int32_t H) { return (size_t)slots_of(T, N, kC) * H * kTile; }
 
 cudaError_t launch_states(const StatePass &p, cudaStream_t s) {
-    CUtensorMap my;
+    CUtensorMap mx, my;
     const int64_t Tm = p.T > 0 ? p.T : 1;
-    if (!make_tile_map_bf16_128(&my, p.y, Tm, p.Hy, kRows)) return cudaErrorInvalidValue;
+    if (!make_tile_map_bf16_128(&mx, p.x, Tm, p.H, kRows) || !make_tile_map_bf16_128(&my, p.y, Tm, p.Hy, kRows))
+        return cudaErrorInvalidValue;
     if (p.seg) {
-        cudaError_t e = launch<false>(my, p, s);
+        cudaError_t e = launch<false>(mx, my, p, s);
         if (e != cudaSuccess) return e;
         Pass scan{};
         scan.H = p.H; scan.Da = kD; scan.Dc = kD; scan.log_decay = p.log_decay; scan.reverse = p.reverse;
@@ -491,7 +500,7 @@ cudaError_t launch_states(const StatePass &p, cudaStream_t s) {
         e = launch_scan(scan, s);
         if (e != cudaSuccess) return e;
     }
-    return launch<true>(my, p, s);
+    return launch<true>(mx, my, p, s);
 }
 
 }  // namespace linear
