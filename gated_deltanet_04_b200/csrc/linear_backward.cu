@@ -303,7 +303,7 @@ __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t 
         warp_arrive(&ms->item_empty[n & 1]);
         for (int g = 0; g < G; ++g, ++u) {
             const int h = im.j * G + g;
-            const float l2 = p.log_decay[h] * kLog2e;
+            const float l2 = log2_decay(p.log_decay, h);
             if (im.L < kC) {
                 ok = ok && wait(ms->full[B_V], u) && wait(ms->full[B_DO], u) && wait(ms->full[B_K], n) &&
                      wait(ms->full[B_Q], n);

@@ -217,7 +217,7 @@ __device__ void epilogue(const OutPass &p, uint8_t *sm, Misc *ms, uint32_t tmem,
         tc_fence_after_sync();
         for (int g = 0; g < G; ++g, ++u, r += 2) {
             const int h = im.j * G + g;
-            const float l2 = p.log_decay[h] * kLog2e;
+            const float l2 = log2_decay(p.log_decay, h);
             if (im.L < kC) {  // V rows of the next sequence: 0 times their NaN would reach every row
                 if (!wait(ms->full_v[r % kRing], r / kRing)) return;
                 uint8_t *v = sm + OFF_RING + (r % kRing) * kTile;

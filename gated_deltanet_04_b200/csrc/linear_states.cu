@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int hy = h / (p.H / p.Hy);
     const int32_t len = (int32_t)(sp.t1 - sp.t0);
     const Walk w{sp.t0, len, (len + kC - 1) / kC, p.reverse};
-    const float l2 = p.log_decay[h] * kLog2e;
+    const float l2 = log2_decay(p.log_decay, h);
     const bool exact = !kDump || (last && p.mT);  // its sum goes into an fp32 state
 
     if (tid == 0) {
@@ -375,9 +375,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 64; c += 32) {  // a whole 128-byte line per thread at a time
             float v[32];
 #pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-                const float4 f = src ? *reinterpret_cast<const float4 *>(src + c + x) : make_float4(0.f, 0.f, 0.f, 0.f);
-                v[x] = f.x; v[x + 1] = f.y; v[x + 2] = f.z; v[x + 3] = f.w;
+            for (int x = 0; x < 32; x += 8) {
+                uint32_t u[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                if (src) load_b256(src + c + x, u);
+#pragma unroll
+                for (int y = 0; y < 8; ++y) v[x + y] = __uint_as_float(u[y]);
             }
             tmem_st32(trow + TM_S + c, v);
             if (kDump && w.nch > 0) {

@@ -67,11 +67,36 @@ __device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a_tmem, uint32_t b, 
     for (int ks = 0; ks < 8; ++ks) mma_f16_ts(d, a_tmem + 8 * ks, step_m(db, ks), IDESC_KM, acc || ks);
 }
 
-// 32 bytes in one store: a whole memory sector per thread.
+// 32 bytes in one access, a whole memory sector per thread, where the address is
+// a multiple of 32 (the caller's arrays are multiples of 16).
 __device__ __forceinline__ void store_b256(void *p, const uint32_t (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+    if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        static_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+__device__ __forceinline__ void load_b256(const void *p, uint32_t (&v)[8]) {
+    if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "l"(p)
+                     : "memory");
+    } else {
+        const uint4 a = static_cast<const uint4 *>(p)[0], b = static_cast<const uint4 *>(p)[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+}
+
+// A head's log2(lam), no further down than where every power of it but the 0th is
+// zero in fp32 anyway: infinity times no tokens must not arise.
+__device__ __forceinline__ float log2_decay(const float *log_decay, int h) {
+    const float x = log_decay[h] * kLog2e;
+    return x < -1000.f ? -1000.f : x;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {

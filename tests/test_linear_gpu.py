@@ -338,6 +338,98 @@ def test_decode_step(shape, N):
     check_step(c, o.t, st.t)
 
 
+def at_16(t):
+    """A copy of t at an address that is a multiple of 16 but not of 32."""
+    if t is None:
+        return None
+    n = t.numel() * t.element_size()
+    buf = torch.empty(n + 64, dtype=torch.uint8, device=DEV)
+    off = 16 if buf.data_ptr() % 32 == 0 else 0
+    view = buf[off:off + n].view(t.dtype).view(t.shape)
+    assert view.data_ptr() % 32 == 16
+    return view.copy_(t)
+
+
+def test_arrays_aligned_to_16_bytes_only():
+    for shape in [(1, 2, 64, 64, F32), (2, 6, 128, 128, BF)]:
+        c = make([300, 5, 129], *shape, seed=71)
+        want, wantg = run_prefill(c), run_backward(c)
+        a = [at_16(c[x].to(DEV)) for x in ("q", "k", "v", "g", "s0")]
+        cu, do, dsT = at_16(c["cu"].to(DEV)), at_16(c["do"].to(DEV)), at_16(c["dsT"].to(DEV))
+        N, T = len(c["lens"]), sum(c["lens"])
+        size = (N, T, *shape[:4])
+        f, b = gdn.gdn_linear_prefill_workspace_bytes, gdn.gdn_linear_prefill_backward_workspace_bytes
+        ws = [at_16(torch.zeros(max(x(*size, dtype=shape[4]), 16), dtype=torch.uint8, device=DEV)) for x in (f, b)]
+        o, sT = at_16(want[0]), at_16(want[1])
+        gdn.gdn_linear_prefill(*a, cu, scale=c["scale"], o=o.zero_(), final_state=sT.zero_(), workspace=ws[0])
+        assert torch.equal(o, want[0]) and torch.equal(sT, want[1])
+        outs = [at_16(x).zero_() for x in wantg]
+        gdn.gdn_linear_prefill_backward(do, *a, cu, dfinal_state=dsT, scale=c["scale"], dq=outs[0], dk=outs[1],
+                                        dv=outs[2], dinitial_state=outs[3], workspace=ws[1])
+        assert all(torch.equal(x, y) for x, y in zip(outs, wantg))
+        st = at_16(c["s0"].to(DEV))
+        o = gdn.gdn_linear_decode_step(*[at_16(x[:3]) for x in a[:3]], a[3], st, scale=c["scale"])
+        st2 = dev(c["s0"])
+        assert torch.equal(o, gdn.gdn_linear_decode_step(*[x[:3].contiguous() for x in a[:3]], a[3], st2,
+                                                         scale=c["scale"]))
+        assert torch.equal(st, st2)
+
+
+def test_a_new_request_does_not_read_its_slot():
+    """reset: whatever the slot held, NaN included, the result is that of zeros."""
+    for shape in [(1, 2, 64, 64, F32), (1, 2, 128, 128, BF)]:
+        c = make([40, 130], *shape, seed=73)
+        pool = torch.full((3, *c["s0"].shape[1:]), float("nan"), device=DEV)
+        slots, reset = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([2, 0], [1, 1]))
+        a = [dev(c[x]) for x in ("q", "k", "v", "g")]
+        o = gdn.gdn_linear_prefill_slots(*a, pool, slots, reset, dev(c["cu"]), scale=c["scale"])
+        c["s0"] = None
+        check_prefill(c, o, pool[[2, 0]])
+        pool.fill_(float("nan"))
+        o = gdn.gdn_linear_decode_step_slots(*[x[:2].contiguous() for x in a[:3]], a[3], pool, slots, reset)
+        assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(pool[[2, 0]]).all())
+
+
+def test_extreme_decays_and_scales():
+    """Decays of fp32's whole finite range and a zero scale give finite results
+    equal to the oracle's."""
+    for shape in [(1, 4, 64, 64, F32), (1, 4, 128, 128, BF)]:
+        c = make([260, 33], *shape, seed=79)
+        c["g"] = torch.tensor([-3.4e38, -90.0, -1e-30, 0.0])
+        check_prefill(c, *run_prefill(c))
+        check_backward(c, run_backward(c))
+        c["scale"] = 0.0
+        o, _ = run_prefill(c)
+        assert not bool(o.any())
+        assert not bool(run_backward(c)[0].any())
+
+
+def test_more_than_2_to_31_elements():
+    """v of 400,000 tokens and 48 heads has more than 2^31 elements: the last
+    tokens' results are those of a run over the last 2,048, before which the
+    decay (at most e^-0.5 a token) leaves nothing in fp32."""
+    T, Hqk, Hv, D, tail = 400_000, 1, 48, 128, 2048
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    gen = torch.Generator(device=DEV).manual_seed(83)
+    r = lambda *s: torch.randn(*s, generator=gen, device=DEV, dtype=BF)
+    q, k, v, do = r(T, Hqk, D), r(T, Hqk, D), r(T, Hv, D), r(T, Hv, D)
+    assert v.numel() > 1 << 31
+    g = torch.full((Hv,), -0.5, device=DEV)
+    o, sT = gdn.gdn_linear_prefill(q, k, v, g, scale=D ** -0.5)
+    # chunks of 128 tokens from the sequence's start: the tail starts on one
+    t0 = (T - tail) // 128 * 128
+    o2, s2 = gdn.gdn_linear_prefill(q[t0:], k[t0:], v[t0:], g, scale=D ** -0.5)
+    half = t0 + 1024
+    assert torch.equal(o[half:], o2[1024:])
+    assert float((sT - s2).abs().max()) <= 2.0 ** -20 * float(s2.abs().max())
+    del o, o2
+    dq, dk, dv, _ = gdn.gdn_linear_prefill_backward(do, q, k, v, g, scale=D ** -0.5)
+    gq, gk, gv, _ = gdn.gdn_linear_prefill_backward(do[t0:], q[t0:], k[t0:], v[t0:], g, scale=D ** -0.5)
+    for x, y in ((dq, gq), (dk, gk), (dv, gv)):
+        assert torch.equal(x[half:], y[1024:])
+
+
 def test_bad_slots_are_reported_and_write_nothing():
     for shape in [(1, 2, 64, 64, F32), (1, 2, 128, 128, BF)]:
         Hqk, Hv, Dk, Dv, dt = shape
