@@ -245,22 +245,28 @@ __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t 
             for (int x = 0; x < 16; ++x) out[x] = pack_bf16(v[2 * x], v[2 * x + 1]);
         }
     };
-    // this thread's 32 columns of an accumulator to its token's row of dst; product `release`
-    // (>= 0) is done with once they are read
-    auto write = [&](uint32_t col, void *dst, int64_t t0, int L, int H, int h, int release) {
+    // this thread's 32 columns of an accumulator as 16 words of bf16 pairs, and into its token's
+    // row of dst
+    auto read = [&](uint32_t col, uint32_t (&w)[16]) {
         float v[32];
         tmem_ld32(tcol + col, v);
         tmem_wait_ld();
-        if (release >= 0) done(release);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) w[x] = pack_bf16(v[2 * x], v[2 * x + 1]);
+    };
+    auto write = [&](const uint32_t (&w)[16], void *dst, int64_t t0, int L, int H, int h) {
         if (row >= L || !ok) return;
         __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(dst) + ((t0 + row) * H + h) * (int64_t)kD + 32 * cg;
 #pragma unroll
-        for (int c = 0; c < 32; c += 16) {
-            uint32_t w[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) w[x] = pack_bf16(v[c + 2 * x], v[c + 2 * x + 1]);
-            store_b256(d + c, w);
-        }
+        for (int c = 0; c < 16; c += 8)
+            store_b256(d + 2 * c, {w[c], w[c + 1], w[c + 2], w[c + 3], w[c + 4], w[c + 5], w[c + 6], w[c + 7]});
+    };
+    auto write_item = [&](const Item &im) {
+        uint32_t w[16];
+        read(TM_DQ, w);
+        write(w, p.dq, im.t0, im.L, p.Hqk, im.j);
+        read(TM_DK, w);
+        write(w, p.dk, im.t0, im.L, p.Hqk, im.j);
     };
     // acc = (first ? 0 : acc) + f T
     auto add = [&](uint32_t acc, uint32_t T, float f, bool first) {
@@ -327,10 +333,6 @@ __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t 
             uint32_t out[16];
 
             product(0);  // T0 = K Q^T, and all of the previous item
-            if (g == 0 && prev.L >= 0) {
-                write(TM_DQ, p.dq, prev.t0, prev.L, p.Hqk, prev.j, -1);
-                write(TM_DK, p.dk, prev.t0, prev.L, p.Hqk, prev.j, -1);
-            }
             masked(false, l2, out);
             quad_barrier(quad);  // T0's rows have been read: P^T takes their place
             tmem_st16u(trow + TM_T0 + 16 * cg, out);
@@ -339,7 +341,10 @@ __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t 
             add(TM_T1, TM_T1, fj, true);
             done(1);
             product(2);  // T1 = dv
-            write(TM_T1, p.dv, im.t0, im.L, p.Hv, h, 2);
+            uint32_t dv[16];
+            read(TM_T1, dv);
+            done(2);
+            write(dv, p.dv, im.t0, im.L, p.Hv, h);
             product(3);  // T0 = dO V^T
             masked(true, l2, out);
 #pragma unroll
@@ -348,6 +353,8 @@ __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t 
                     make_uint4(out[4 * x], out[4 * x + 1], out[4 * x + 2], out[4 * x + 3]);
             fence_proxy_async_smem();
             done(3);
+            // here, not at product 0, where every later product of the head waits (4 % slower)
+            if (g == 0 && prev.L >= 0) write_item(prev);
             product(4);  // T1 = dO S
             add(TM_DQ, TM_T1, fi, g == 0);
             done(4);
@@ -359,8 +366,7 @@ __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t 
     }
     if (prev.L >= 0) {
         product(0);
-        write(TM_DQ, p.dq, prev.t0, prev.L, p.Hqk, prev.j, -1);
-        write(TM_DK, p.dk, prev.t0, prev.L, p.Hqk, prev.j, -1);
+        write_item(prev);
     }
 }
 
