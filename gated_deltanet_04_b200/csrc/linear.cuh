@@ -126,8 +126,9 @@ struct Decay {
 // Token-recurrent passes for any Da, Dc of 16, 32, 64, 128 and either dtype.
 // `phase` 0: the whole pass; 1: the segments' own sums into p.seg.
 cudaError_t launch_recurrent(const Pass &p, int phase, cudaStream_t s);
-// The states entering every segment, in place of the sums in p.seg.
-cudaError_t launch_scan(const Pass &p, cudaStream_t s);
+// The states entering every segment, in place of the sums in p.seg; of one pass, or of
+// two of the same N, H, Da and Dc.
+cudaError_t launch_scan(const Pass *p, int passes, cudaStream_t s);
 // Segment length for the recurrent passes, or 0 for one segment per sequence.
 int64_t recurrent_seg_len(int32_t N, int64_t T, int32_t H, int32_t Da, int32_t Dc);
 // dst[t][j] = sum of the H / Hout heads of group j, in dst's dtype.

@@ -70,18 +70,17 @@ bool tensor_cores(const Call &c) {
 size_t prefill_bytes(const Call &c) {
     if (check(c) != GDN_OK || check_size(c) != GDN_OK || c.T == 0) return 0;
     if (tensor_cores(c))
-        return gdn::linear::state_dump_bytes(c.N, c.T, c.Hv) + gdn::linear::state_seg_bytes(c.N, c.T, c.Hv);
+        return gdn::linear::state_dump_bytes(c.N, c.T, c.Hv) + gdn::linear::state_seg_bytes(c.N, c.T, c.Hv, 1);
     return seg_bytes(c, gdn::linear::recurrent_seg_len(c.N, c.T, c.Hv, c.Dk, c.Dv));
 }
 
-// Tensor cores: the images of S and of G, and the segment states, which the two
-// state passes share.  Otherwise the three gradients run one after another and
+// Tensor cores: the images of S and of G, and the segment states of each.  Otherwise the three gradients run one after another and
 // share the segment states; dq and dk of v-heads that share a q/k head are
 // summed from fp32 partials.
 size_t backward_bytes(const Call &c) {
     if (check(c) != GDN_OK || check_size(c) != GDN_OK || c.T == 0) return 0;
     if (tensor_cores(c))
-        return 2 * gdn::linear::state_dump_bytes(c.N, c.T, c.Hv) + gdn::linear::state_seg_bytes(c.N, c.T, c.Hv);
+        return 2 * gdn::linear::state_dump_bytes(c.N, c.T, c.Hv) + 2 * gdn::linear::state_seg_bytes(c.N, c.T, c.Hv, 2);
     const size_t a = seg_bytes(c, gdn::linear::recurrent_seg_len(c.N, c.T, c.Hv, c.Dk, c.Dv));
     const size_t b = seg_bytes(c, gdn::linear::recurrent_seg_len(c.N, c.T, c.Hv, c.Dv, c.Dk));
     const size_t part = c.Hv > c.Hqk ? al256((size_t)c.T * c.Hv * c.Dk * 4) : 0;
@@ -94,23 +93,27 @@ cudaError_t run(Pass p, void *ws, cudaStream_t s) {
     p.seg = p.seg_len ? static_cast<float *>(ws) : nullptr;
     if (p.seg) {
         cudaError_t e = gdn::linear::launch_recurrent(p, 1, s);
-        if (e == cudaSuccess) e = gdn::linear::launch_scan(p, s);
+        if (e == cudaSuccess) e = gdn::linear::launch_scan(&p, 1, s);
         if (e != cudaSuccess) return e;
     }
     return gdn::linear::launch_recurrent(p, 0, s);
 }
 
-// A state pass whose workspace holds `dumps` image arrays, then the segment states.
+// State pass `which` of `passes` that run together: the workspace holds their image
+// arrays, then their segment states.
 gdn::linear::StatePass states(const Call &c, const void *x, const void *y, int32_t Hy, const float *log_decay,
-                              float x_scale, bool reverse, const float *m0, float *mT, void *ws, int dumps,
-                              int32_t *err) {
+                              float x_scale, bool reverse, const float *m0, float *mT, void *ws, int which,
+                              int passes, int32_t *err) {
     gdn::linear::StatePass st{};
     st.x = x; st.y = y; st.H = c.Hv; st.Hy = Hy; st.log_decay = log_decay; st.x_scale = x_scale;
     st.reverse = reverse; st.m0 = m0; st.mT = mT; st.cu = c.cu; st.N = c.N; st.T = c.T; st.err = err;
-    st.dump = static_cast<uint8_t *>(ws);
-    st.seg_chunks = gdn::linear::state_seg_chunks(c.N, c.T, c.Hv);
+    const size_t dump = gdn::linear::state_dump_bytes(c.N, c.T, c.Hv);
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    st.dump = base + which * dump;
+    st.seg_chunks = gdn::linear::state_seg_chunks(c.N, c.T, c.Hv, passes);
     if (st.seg_chunks)
-        st.seg = reinterpret_cast<float *>(st.dump + dumps * gdn::linear::state_dump_bytes(c.N, c.T, c.Hv));
+        st.seg = reinterpret_cast<float *>(base + passes * dump +
+                                           which * gdn::linear::state_seg_bytes(c.N, c.T, c.Hv, passes));
     return st;
 }
 
@@ -121,9 +124,9 @@ gdn_status prefill(const void *q, const void *k, const void *v, const float *log
     if (need > 0 && (ws == nullptr || ws_bytes < need)) return GDN_ERR_INVALID_ARGUMENT;
     if (c.N == 0 || (c.T == 0 && sT == nullptr)) return GDN_OK;  // nothing observable to do
     if (tensor_cores(c)) {
-        gdn::linear::StatePass st = states(c, v, k, c.Hqk, log_decay, 1.f, false, s0, sT, ws, 1, err);
+        gdn::linear::StatePass st = states(c, v, k, c.Hqk, log_decay, 1.f, false, s0, sT, ws, 0, 1, err);
         st.map = map;
-        const cudaError_t e = gdn::linear::launch_states(st, s);
+        const cudaError_t e = gdn::linear::launch_states(&st, 1, s);
         if (e != cudaSuccess) return from_cuda(e);
         return from_cuda(gdn::linear::launch_out({q, k, v, o, st.dump, log_decay, scale, c.cu, c.N, c.T, c.Hqk,
                                                   c.Hv, err}, s));
@@ -224,15 +227,14 @@ gdn_status gdn_linear_prefill_backward(const void *dO, const void *q, const void
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (tensor_cores(c)) {
-        gdn::linear::StatePass ps = states(c, v, k, Hqk, log_decay, 1.f, false, initial_state, nullptr, workspace,
-                                           2, dev_error_flag);
-        gdn::linear::StatePass pg = states(c, dO, q, Hqk, log_decay, scale, true, dfinal_state, dinitial_state,
-                                           workspace, 2, dev_error_flag);
-        pg.dump += gdn::linear::state_dump_bytes(N, T, Hv);
-        cudaError_t e = gdn::linear::launch_states(ps, s);
-        if (e == cudaSuccess) e = gdn::linear::launch_states(pg, s);
+        // S and G do not depend on one another: one launch for both
+        const gdn::linear::StatePass sg[2] = {states(c, v, k, Hqk, log_decay, 1.f, false, initial_state, nullptr,
+                                                     workspace, 0, 2, dev_error_flag),
+                                              states(c, dO, q, Hqk, log_decay, scale, true, dfinal_state,
+                                                     dinitial_state, workspace, 1, 2, dev_error_flag)};
+        cudaError_t e = gdn::linear::launch_states(sg, 2, s);
         if (e == cudaSuccess)
-            e = gdn::linear::launch_backward({dO, q, k, v, dq, dk, dv, ps.dump, pg.dump, log_decay, scale,
+            e = gdn::linear::launch_backward({dO, q, k, v, dq, dk, dv, sg[0].dump, sg[1].dump, log_decay, scale,
                                               cu_seqlens, N, T, Hqk, Hv, dev_error_flag}, s);
         return from_cuda(e);
     }

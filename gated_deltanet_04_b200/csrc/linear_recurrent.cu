@@ -224,7 +224,8 @@ __global__ void __launch_bounds__(kThreads)
 // One thread per four elements of a (sequence, head) state: walks the
 // sequence's segments in the pass's order, replacing each segment's sum by the
 // state that enters it.
-__global__ void gdn_linear_scan_kernel(Pass p) {
+__global__ void gdn_linear_scan_kernel(const __grid_constant__ Pass p0, const __grid_constant__ Pass p1) {
+    const Pass &p = blockIdx.z ? p1 : p0;
     const int n = blockIdx.x / p.H, h = blockIdx.x % p.H;
     const int per = p.Dc * p.Da;
     const int x = 4 * (int)(blockIdx.y * blockDim.x + threadIdx.x);
@@ -331,12 +332,14 @@ cudaError_t launch_recurrent(const Pass &p, int phase, cudaStream_t s) {
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_scan(const Pass &p, cudaStream_t s) {
+cudaError_t launch_scan(const Pass *passes, int count, cudaStream_t s) {
+    const Pass &p = passes[0];
     const int64_t units = (int64_t)p.N * p.H;
     if (units <= 0) return cudaSuccess;
     if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int per = p.Dc * p.Da / 4, threads = per < 256 ? per : 256;
-    gdn_linear_scan_kernel<<<dim3((unsigned)units, (unsigned)((per + threads - 1) / threads)), threads, 0, s>>>(p);
+    gdn_linear_scan_kernel<<<dim3((unsigned)units, (unsigned)((per + threads - 1) / threads), count), threads, 0, s>>>(
+        p, passes[count - 1]);
     return cudaGetLastError();
 }
 

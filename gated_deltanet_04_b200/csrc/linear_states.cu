@@ -63,6 +63,12 @@ struct Misc {
 constexpr uint32_t kSmem = OFF_MISC + sizeof(Misc) + 1024;
 static_assert(kSmem <= 232448, "shared memory of an SM");
 
+// A launch's passes (blockIdx.y); all have the same N, T, H, cu and segments.
+struct Passes {
+    CUtensorMap x[2], y[2];
+    StatePass p[2];
+};
+
 // The chunks of a segment in the pass's order: tokens t0 .. t0 + len - 1.
 struct Walk {
     int64_t t0;
@@ -280,13 +286,13 @@ __device__ __forceinline__ void state_barrier() {
 // kDump: the pass proper (images, final state); otherwise the segments' sums.
 template <bool kDump>
 __global__ void __launch_bounds__(kThreads, 1)
-    gdn_linear_states_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
-                             StatePass p) {
+    gdn_linear_states_kernel(const __grid_constant__ Passes passes) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Misc *ms = reinterpret_cast<Misc *>(sm + OFF_MISC);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    const StatePass &p = passes.p[blockIdx.y];
     const int h = blockIdx.x % p.H;
     const int64_t slot = blockIdx.x / p.H;
     const int64_t seg_len = p.seg ? p.seg_chunks * kC : (p.T > 0 ? p.T : 1);
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (w.nch > 0 && exact) convert<3>(w, sm, ms, tlane, group, half, row + 128 * half, p.err);
             else if (w.nch > 0) convert<2>(w, sm, ms, tlane, group, half, row + 128 * half, p.err);
         } else if (cw == kConvWarps) {
-            if (lane == 0) produce(tm_x, tm_y, w, h, hy, sm, ms, p.err);
+            if (lane == 0) produce(passes.x[blockIdx.y], passes.y[blockIdx.y], w, h, hy, sm, ms, p.err);
         } else if (lane == 0) {
             if (exact) multiply<3>(w, smem_u32(sm), tmem, ms, p.err);
             else multiply<2>(w, smem_u32(sm), tmem, ms, p.err);
@@ -449,14 +455,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kDump>
-cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &my, const StatePass &p, cudaStream_t s) {
+cudaError_t launch(const Passes &passes, int count, cudaStream_t s) {
+    const StatePass &p = passes.p[0];
     const int64_t len = p.seg ? p.seg_chunks * kC : (p.T > 0 ? p.T : 1);
     const int64_t blocks = slots_of(p.T, p.N, len) * p.H;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(gdn_linear_states_kernel<kDump>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    gdn_linear_states_kernel<kDump><<<(unsigned)blocks, kThreads, kSmem, s>>>(mx, my, p);
+    gdn_linear_states_kernel<kDump><<<dim3((unsigned)blocks, count), kThreads, kSmem, s>>>(passes);
     return cudaGetLastError();
 }
 
@@ -473,36 +480,44 @@ int device_sms() {
 // long as the share, so that one wave of 148 CTAs has them all.  Measured with 48
 // heads and one sequence: 4,096 tokens 72 us with and 77 without, 65,536 tokens 550
 // and 800; segments for four waves 664.
-int64_t state_seg_chunks(int32_t N, int64_t T, int32_t H) {
-    const int64_t longest = T / kC + 1, all = (T / kC + N) * H, share = all / 148;
+int64_t state_seg_chunks(int32_t N, int64_t T, int32_t H, int passes) {
+    const int64_t longest = T / kC + 1, all = (T / kC + N) * H * passes, share = all / 148;
     if (N <= 0 || T <= 0 || longest <= 3 * share + 2) return 0;
     const int64_t len = (all + 147) / 148;
     return len < 4 ? 4 : len;
 }
 
-size_t state_seg_bytes(int32_t N, int64_t T, int32_t H) {
-    const int64_t c = state_seg_chunks(N, T, H);
+size_t state_seg_bytes(int32_t N, int64_t T, int32_t H, int passes) {
+    const int64_t c = state_seg_chunks(N, T, H, passes);
     return c ? (size_t)slots_of(T, N, c * kC) * H * kD * kD * 4 : 0;
 }
 
 size_t state_dump_bytes(int32_t N, int64_t T, int32_t H) { return (size_t)slots_of(T, N, kC) * H * kTile; }
 
-cudaError_t launch_states(const StatePass &p, cudaStream_t s) {
-    CUtensorMap mx, my;
-    const int64_t Tm = p.T > 0 ? p.T : 1;
-    if (!make_tile_map_bf16_128(&mx, p.x, Tm, p.H, kRows) || !make_tile_map_bf16_128(&my, p.y, Tm, p.Hy, kRows))
-        return cudaErrorInvalidValue;
-    if (p.seg) {
-        cudaError_t e = launch<false>(mx, my, p, s);
+cudaError_t launch_states(const StatePass *p, int passes, cudaStream_t s) {
+    Passes all{};
+    for (int i = 0; i < passes; ++i) {
+        const int64_t Tm = p[i].T > 0 ? p[i].T : 1;
+        if (!make_tile_map_bf16_128(&all.x[i], p[i].x, Tm, p[i].H, kRows) ||
+            !make_tile_map_bf16_128(&all.y[i], p[i].y, Tm, p[i].Hy, kRows))
+            return cudaErrorInvalidValue;
+        all.p[i] = p[i];
+    }
+    if (p[0].seg) {
+        cudaError_t e = launch<false>(all, passes, s);
         if (e != cudaSuccess) return e;
-        Pass scan{};
-        scan.H = p.H; scan.Da = kD; scan.Dc = kD; scan.log_decay = p.log_decay; scan.reverse = p.reverse;
-        scan.m0 = p.m0; scan.map = p.map; scan.cu = p.cu; scan.N = p.N; scan.T = p.T; scan.err = p.err;
-        scan.seg = p.seg; scan.seg_len = p.seg_chunks * kC;
-        e = launch_scan(scan, s);
+        Pass scan[2];
+        for (int i = 0; i < passes; ++i) {
+            const StatePass &a = p[i];
+            Pass &b = scan[i] = Pass{};
+            b.H = a.H; b.Da = kD; b.Dc = kD; b.log_decay = a.log_decay; b.reverse = a.reverse;
+            b.m0 = a.m0; b.map = a.map; b.cu = a.cu; b.N = a.N; b.T = a.T; b.err = a.err;
+            b.seg = a.seg; b.seg_len = a.seg_chunks * kC;
+        }
+        e = launch_scan(scan, passes, s);
         if (e != cudaSuccess) return e;
     }
-    return launch<true>(mx, my, p, s);
+    return launch<true>(all, passes, s);
 }
 
 }  // namespace linear

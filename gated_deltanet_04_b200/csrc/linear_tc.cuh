@@ -166,12 +166,13 @@ struct StatePass {
     uint8_t *dump;
 };
 
-// Workspace of a StatePass besides its dump; the dump's bytes.
-int64_t state_seg_chunks(int32_t N, int64_t T, int32_t H);  // 0: one segment per sequence
-size_t state_seg_bytes(int32_t N, int64_t T, int32_t H);
+// Workspace of a StatePass besides its dump, of `passes` that run together; the dump's bytes.
+int64_t state_seg_chunks(int32_t N, int64_t T, int32_t H, int passes);  // 0: one segment per sequence
+size_t state_seg_bytes(int32_t N, int64_t T, int32_t H, int passes);    // of each pass
 size_t state_dump_bytes(int32_t N, int64_t T, int32_t H);
-// Runs the pass (segment sums and scan first when p.seg is set).
-cudaError_t launch_states(const StatePass &p, cudaStream_t s);
+// Runs one pass, or two of the same N, T, H, cu and seg_chunks side by side (segment
+// sums and scan first when seg is set).
+cudaError_t launch_states(const StatePass *p, int passes, cudaStream_t s);
 
 struct OutPass {
     const void *q, *k, *v;
