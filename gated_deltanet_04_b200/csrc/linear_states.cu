@@ -41,22 +41,18 @@ constexpr uint32_t kStage = 2 * kPart;       // x, y
 constexpr uint32_t OFF_IMAGE = kRing * kStage;
 constexpr uint32_t OFF_MISC = OFF_IMAGE + kTile;
 
-// Tensor memory columns: the state, the sum; then with two parts a second sum
-// and two buffers of 2 x 32 columns, with three two buffers of 3 x 32.
-constexpr uint32_t TM_S = 0, TM_SUM = 128;
-template <int kParts>
-struct Columns {
-    static constexpr int kSums = kParts == 2 ? 2 : 1;
-    static constexpr uint32_t kFirst = TM_SUM + 128 * kSums;
-    static constexpr uint32_t parts(int buf) { return kFirst + buf * kParts * 32; }
-};
-static_assert(Columns<2>::parts(2) <= 512 && Columns<3>::parts(2) <= 512, "tensor memory");
+// Tensor memory columns: the state, two sums, and a buffer of two parts (32 columns
+// each) per converting group.  A third part takes the first one's place once that has
+// been multiplied.
+constexpr uint32_t TM_S = 0, TM_SUM = 128, TM_PARTS = TM_SUM + 256;
+constexpr int kSums = 2;
 
 struct Misc {
     // of token pairs, a whole chunk's and the partial chunk's: as two bf16 parts, and in fp32
     alignas(16) uint32_t weight[2][2][kC / 2];
     alignas(16) float2 weight32[2][kC / 2];
-    uint64_t raw_full[kRing], raw_empty[kRing], part_full[2], part_empty[2], sum_full[2], sum_empty[2], drain;
+    uint64_t raw_full[kRing], raw_empty[kRing], part_full[2], part_empty[2], third_full[2], first_empty[2],
+        sum_full[2], sum_empty[2], drain;
     uint32_t tmem;
     volatile int32_t abort;
 };
@@ -163,7 +159,7 @@ __device__ void convert(const Walk &w, uint8_t *sm, Misc *ms, uint32_t tlane, in
     uint32_t at_q[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) at_q[q] = (col >> 6) * kHalf + sw128(32 * half + 2 * q + odd, (col & 63) * 2);
-    const uint32_t dst = tlane + Columns<kParts>::parts(group) + 16 * half;
+    const uint32_t dst = tlane + TM_PARTS + 64 * group + 16 * half;
     At a{0, 0};
     if (group == 1) a = w.length(0) > kRows ? At{0, 1} : At{1, 0};
     for (uint32_t r = group; a.it < w.nch; r += 2) {
@@ -184,9 +180,10 @@ __device__ void convert(const Walk &w, uint8_t *sm, Misc *ms, uint32_t tlane, in
 #pragma unroll
         for (int q = 0; q < 16; ++q)  // this lane's column, two tokens
             in[q] = __byte_perm(in[q], __shfl_xor_sync(0xffffffffu, in[q], 1), swap);
+        uint32_t lo[16];
 #pragma unroll
         for (int q0 = 0; q0 < 16; q0 += 8) {
-            uint32_t hi[8], mid[8], lo[8];
+            uint32_t hi[8], mid[8];
             if constexpr (kParts == 2) {
 #pragma unroll
                 for (int q = 0; q < 8; q += 4) {
@@ -212,15 +209,15 @@ __device__ void convert(const Walk &w, uint8_t *sm, Misc *ms, uint32_t tlane, in
                         hi[q + e] = pack_bf16(left2);
                         left2 = ffma2(unpack_bf16(hi[q + e]), minus, left2);
                         mid[q + e] = pack_bf16(left2);
-                        lo[q + e] = pack_bf16(ffma2(unpack_bf16(mid[q + e]), minus, left2));
+                        lo[q0 + q + e] = pack_bf16(ffma2(unpack_bf16(mid[q + e]), minus, left2));
                     }
                 }
             }
             // as late as can be: the MMAs of the other group's stage cover what follows
             if (q0 == 0 && r >= 2 && !role_wait(&ms->part_empty[group], ((r >> 1) - 1) & 1, &ms->abort, err)) return;
+            tc_fence_after_sync();
             tmem_st8u(dst + q0, hi);
             tmem_st8u(dst + 32 + q0, mid);
-            if (kParts == 3) tmem_st8u(dst + 64 + q0, lo);
         }
         if (left < kRows) {  // y of the next sequence: 0 times its NaN would reach this sum
             uint8_t *y = sm + b * kStage + kPart;
@@ -232,6 +229,14 @@ __device__ void convert(const Walk &w, uint8_t *sm, Misc *ms, uint32_t tlane, in
         tmem_wait_st();
         tc_fence_before_sync();
         warp_arrive(&ms->part_full[group]);
+        if (kParts == 3) {
+            if (!role_wait(&ms->first_empty[group], (r >> 1) & 1, &ms->abort, err)) return;
+            tc_fence_after_sync();
+            tmem_st16u(dst, lo);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            warp_arrive(&ms->third_full[group]);
+        }
         a = advance(a);
     }
 }
@@ -240,7 +245,6 @@ __device__ void convert(const Walk &w, uint8_t *sm, Misc *ms, uint32_t tlane, in
 template <int kParts>
 __device__ void multiply(const Walk &w, uint32_t sbase, uint32_t tmem, Misc *ms, int32_t *err) {
     uint32_t r = 0, b = 0, lap = 0;  // stages so far; the ring's stage and lap
-    constexpr int kSums = Columns<kParts>::kSums;
     const uint64_t y0 = desc_m(sbase + kPart, kHalf);
     bool ok = true;
     for (int it = 0; ok && it < w.nch; ++it) {
@@ -257,12 +261,20 @@ __device__ void multiply(const Walk &w, uint32_t sbase, uint32_t tmem, Misc *ms,
                 break;
             tc_fence_after_sync();
             const uint64_t y = y0 + b * (kStage >> 4);
-            const uint32_t x = tmem + Columns<kParts>::parts(buf);
-#pragma unroll
-            for (int k = 0; k < kParts; ++k)
+            const uint32_t x = tmem + TM_PARTS + 64 * buf;
+            auto part = [&](uint32_t a, bool first) {
 #pragma unroll
                 for (int ks = 0; ks < kRows / 16; ++ks)
-                    mma_f16_ts(d, x + 32 * k + 8 * ks, step_m(y, ks), IDESC_KM, s || k || ks);
+                    mma_f16_ts(d, a + 8 * ks, step_m(y, ks), IDESC_KM, !first || ks);
+            };
+            part(x, s == 0);
+            if (kParts == 3) mma_commit(&ms->first_empty[buf]);
+            part(x + 32, false);
+            if (kParts == 3) {
+                if (!(ok = role_wait(&ms->third_full[buf], (r >> 1) & 1, &ms->abort, err))) break;
+                tc_fence_after_sync();
+                part(x, false);
+            }
             mma_commit(&ms->raw_empty[b]);
             mma_commit(&ms->part_empty[buf]);
             ++r;
@@ -315,6 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ms->part_full[b], kGroup);
             mbar_init(&ms->part_empty[b], 1);
+            mbar_init(&ms->third_full[b], kGroup);
+            mbar_init(&ms->first_empty[b], 1);
             mbar_init(&ms->sum_full[b], 1);
             mbar_init(&ms->sum_empty[b], kStateWarps);
         }
@@ -396,12 +410,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         if (kDump && w.nch > 0) store_image(0);
         const float dec_full = exp2f(l2 * (float)kC);
-        const int sums = exact ? Columns<3>::kSums : Columns<2>::kSums;
         bool ok = true;
         for (int it = 0; it < w.nch; ++it) {
             // every warp goes on after a wait given up, so that the barriers stay whole
-            const int sum = it % sums;
-            if (ok) ok = role_wait(&ms->sum_full[sum], (it / sums) & 1, &ms->abort, p.err);
+            const int sum = it % kSums;
+            if (ok) ok = role_wait(&ms->sum_full[sum], (it / kSums) & 1, &ms->abort, p.err);
             tc_fence_after_sync();
             const bool more = kDump && it + 1 < w.nch;
             if (more) {
