@@ -24,6 +24,8 @@
 // segments (ceil((b-a)/s) <= floor(b/s) - floor(a/s) + 1), T/seg_len + N in all.
 #pragma once
 
+#include <utility>
+
 #include "gdn_internal.cuh"
 
 namespace gdn {
@@ -56,6 +58,34 @@ struct Pass {
     float *seg;                 // [seg slots][H][Dc][Da], or null: one segment per sequence
     int64_t seg_len;
 };
+
+// Kernels of one call that follow one another on its stream start early: launch_after
+// lets a kernel's CTAs on to SMs as the one before it leaves them, and they wait
+// (prior_done) before they touch anything that an earlier kernel of the call writes.
+// Every CTA waits, those with nothing to do too, so that a kernel's end means that all
+// before it have ended; and a kernel lets the next one on only once its own CTAs hold
+// what they need (next_may_start).  A call's first kernel is launched plainly, and so
+// are the token-recurrent ones: the wait cost their register allocation 5%.  (4,096
+// tokens, 48 heads, four kernels: 115.5 us without, 107.8 with.)
+__device__ __forceinline__ void prior_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), bool after, dim3 grid, int threads, size_t smem, cudaStream_t s,
+                         A &&...args) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = after ? 1 : 0;
+    cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+    return cudaGetLastError();
+}
 
 // First slot of sequence n among slots of `len` tokens.
 __device__ __forceinline__ int64_t slot_base(const int32_t *cu, int n, int64_t len) {

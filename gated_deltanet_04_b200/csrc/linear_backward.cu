@@ -403,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = ms->tmem;
+    prior_done();
     if (warp == kEpiThreads / 32) {
         if (lane == 0) produce(maps, p, items, sm, ms, G);
     } else if (warp == kEpiThreads / 32 + 1) {
@@ -428,8 +429,8 @@ cudaError_t launch_backward(const BackwardPass &p, cudaStream_t s) {
                                          kSmem);
     if (e != cudaSuccess) return e;
     const int64_t items = slots_of(p.T, p.N, kC) * p.Hqk, sms = device_sms();
-    gdn_linear_backward_kernel<<<(unsigned)(items < sms ? items : sms), kThreads, kSmem, s>>>(m, p, items);
-    return cudaGetLastError();
+    return launch_after(gdn_linear_backward_kernel, true, dim3((unsigned)(items < sms ? items : sms)), kThreads, kSmem, s,
+                        m, p, items);
 }
 
 }  // namespace linear

@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = ms->tmem;
+    prior_done();
     if (warp == kEpiThreads / 32) {
         if (lane == 0) produce(tm_q, tm_k, tm_v, p, items, sm, ms, G);
     } else if (warp == kEpiThreads / 32 + 1) {
@@ -302,8 +303,8 @@ cudaError_t launch_out(const OutPass &p, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(gdn_linear_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int64_t items = slots_of(p.T, p.N, kC) * p.Hqk, sms = device_sms();
-    gdn_linear_out_kernel<<<(unsigned)(items < sms ? items : sms), kThreads, kSmem, s>>>(mq, mk, mv, p, items);
-    return cudaGetLastError();
+    return launch_after(gdn_linear_out_kernel, true, dim3((unsigned)(items < sms ? items : sms)), kThreads, kSmem, s,
+                        mq, mk, mv, p, items);
 }
 
 }  // namespace linear

@@ -226,6 +226,8 @@ __global__ void __launch_bounds__(kThreads)
 // state that enters it.
 __global__ void gdn_linear_scan_kernel(const __grid_constant__ Pass p0, const __grid_constant__ Pass p1) {
     const Pass &p = blockIdx.z ? p1 : p0;
+    next_may_start();
+    prior_done();
     const int n = blockIdx.x / p.H, h = blockIdx.x % p.H;
     const int per = p.Dc * p.Da;
     const int x = 4 * (int)(blockIdx.y * blockDim.x + threadIdx.x);
@@ -338,9 +340,9 @@ cudaError_t launch_scan(const Pass *passes, int count, cudaStream_t s) {
     if (units <= 0) return cudaSuccess;
     if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int per = p.Dc * p.Da / 4, threads = per < 256 ? per : 256;
-    gdn_linear_scan_kernel<<<dim3((unsigned)units, (unsigned)((per + threads - 1) / threads), count), threads, 0, s>>>(
-        p, passes[count - 1]);
-    return cudaGetLastError();
+    return launch_after(gdn_linear_scan_kernel, true,
+                        dim3((unsigned)units, (unsigned)((per + threads - 1) / threads), count), threads, 0, s, p,
+                        passes[count - 1]);
 }
 
 // Enough segments for about eight of the 128-thread CTAs on each of 148 SMs,

@@ -310,9 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t seg_len = p.seg ? p.seg_chunks * kC : (p.T > 0 ? p.T : 1);
     if (tid == kThreads - 1) check_range(p.cu, p.N, p.T, slot, p.err);
     Span sp;
-    if (!find_span(p.cu, p.N, p.T, seg_len, slot, p.err, sp)) return;
-    const bool last = p.reverse ? sp.s == 0 : sp.s == sp.count - 1;  // in the pass's order
-    if (!kDump && last) return;  // nothing starts from its sum
+    const bool some = find_span(p.cu, p.N, p.T, seg_len, slot, p.err, sp);
+    const bool last = some && (p.reverse ? sp.s == 0 : sp.s == sp.count - 1);  // in the pass's order
+    if (!some || (!kDump && last)) {  // nothing starts from a last segment's sum
+        prior_done();
+        return;
+    }
     const int hy = h / (p.H / p.Hy);
     const int32_t len = (int32_t)(sp.t1 - sp.t0);
     const Walk w{sp.t0, len, (len + kC - 1) / kC, p.reverse};
@@ -348,6 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = ms->tmem;
+    next_may_start();
+    prior_done();
 
     if (warp >= kStateWarps) {
         const int cw = warp - kStateWarps;
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kDump>
-cudaError_t launch(const Passes &passes, int count, cudaStream_t s) {
+cudaError_t launch(const Passes &passes, int count, bool after, cudaStream_t s) {
     const StatePass &p = passes.p[0];
     const int64_t len = p.seg ? p.seg_chunks * kC : (p.T > 0 ? p.T : 1);
     const int64_t blocks = slots_of(p.T, p.N, len) * p.H;
@@ -476,8 +481,8 @@ cudaError_t launch(const Passes &passes, int count, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(gdn_linear_states_kernel<kDump>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    gdn_linear_states_kernel<kDump><<<dim3((unsigned)blocks, count), kThreads, kSmem, s>>>(passes);
-    return cudaGetLastError();
+    return launch_after(gdn_linear_states_kernel<kDump>, after, dim3((unsigned)blocks, count), kThreads, kSmem, s,
+                        passes);
 }
 
 }  // namespace
@@ -517,7 +522,7 @@ cudaError_t launch_states(const StatePass *p, int passes, cudaStream_t s) {
         all.p[i] = p[i];
     }
     if (p[0].seg) {
-        cudaError_t e = launch<false>(all, passes, s);
+        cudaError_t e = launch<false>(all, passes, false, s);
         if (e != cudaSuccess) return e;
         Pass scan[2];
         for (int i = 0; i < passes; ++i) {
@@ -530,7 +535,7 @@ cudaError_t launch_states(const StatePass *p, int passes, cudaStream_t s) {
         e = launch_scan(scan, passes, s);
         if (e != cudaSuccess) return e;
     }
-    return launch<true>(all, passes, s);
+    return launch<true>(all, passes, p[0].seg != nullptr, s);
 }
 
 }  // namespace linear
