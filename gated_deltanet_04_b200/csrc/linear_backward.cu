@@ -42,6 +42,7 @@ struct Item {
 };
 
 struct Misc {
+    float before[32];    // read, not used: entries -31 .. -1 of the first table
     float up[2][4][32];  // per head (in turn) and lane quarter: lam^0 .. lam^31
     uint64_t full[kBufs], empty[kBufs];
     uint64_t item_full[2], item_empty[2];
@@ -56,7 +57,7 @@ static_assert(kSmem <= 232448, "shared memory of an SM");
 constexpr uint32_t TM_DQ = 0, TM_DK = 128, TM_T0 = 256, TM_T1 = 384;
 
 struct Maps {
-    CUtensorMap q, k, v, g;  // g: dO
+    CUtensorMap q, k, v, g, dq, dk, dv;  // g: dO
 };
 
 // Tiles, in the order in which the head before lets go of their buffers.
@@ -195,7 +196,10 @@ __device__ __forceinline__ bool any_gave_up(bool ok) {
     return any != 0;
 }
 
-__device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t tmem, int G) {
+// All of the epilogue's threads.
+__device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 6, %0;" ::"n"(kEpiThreads) : "memory"); }
+
+__device__ void epilogue(const Maps &m, const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t tmem, int G) {
     volatile int32_t *abort = &ms->abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, cg = warp >> 2;
     const int row = quad * 32 + lane;  // token of the chunk; columns 32 cg ..
@@ -236,10 +240,11 @@ __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t 
                 out[x / 2 + 1] = pack_bf16(fmul2(make_float2(v[x + 2], v[x + 3]), fmul2(w1, f2)));
             }
         } else {
+            const float *w = lower ? up + lane : up - lane;  // lam^|row - column| where it is wanted
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
-                const int d = lower ? lane - x : x - lane;
-                v[x] = d >= 0 ? v[x] * (p.scale * up[d & 31]) : 0.f;
+                const float f = p.scale * w[lower ? -x : x];
+                v[x] = (lower ? x <= lane : x >= lane) ? v[x] * f : 0.f;
             }
 #pragma unroll
             for (int x = 0; x < 16; ++x) out[x] = pack_bf16(v[2 * x], v[2 * x + 1]);
@@ -260,6 +265,30 @@ __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t 
 #pragma unroll
         for (int c = 0; c < 16; c += 8)
             store_b256(d + 2 * c, {w[c], w[c + 1], w[c + 2], w[c + 3], w[c + 4], w[c + 5], w[c + 6], w[c + 7]});
+    };
+    // these 16 words of every thread to P's place, as a tile
+    auto to_tile = [&](const uint32_t (&w)[16]) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<uint4 *>(sm + OFF_P + (cg >> 1) * kSub + sw128(row, 64 * (cg & 1) + 16 * x)) =
+                make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+        fence_proxy_async_smem();
+    };
+    // a whole chunk's tile to dst by TMA, through P's place while no P' is in it (rows from
+    // registers are 64 bytes a thread, a line each, and hold up the SM's other accesses)
+    auto clear_tile = [&] {
+        if (tid == 0) bulk_wait_read_all();
+        epi_barrier();
+    };
+    auto store_tile = [&](const uint32_t (&w)[16], const CUtensorMap &dst, int64_t t0, int h) {
+        clear_tile();
+        to_tile(w);
+        epi_barrier();
+        if (tid == 0 && ok) {
+            tma_store_3d(&dst, sm + OFF_P, 0, h, (int32_t)t0);
+            tma_store_3d(&dst, sm + OFF_P + kSub, 64, h, (int32_t)t0);
+            bulk_commit();
+        }
     };
     auto write_item = [&](const Item &im) {
         uint32_t w[16];
@@ -337,24 +366,29 @@ __device__ void epilogue(const BackwardPass &p, uint8_t *sm, Misc *ms, uint32_t 
             quad_barrier(quad);  // T0's rows have been read: P^T takes their place
             tmem_st16u(trow + TM_T0 + 16 * cg, out);
             done(0);
+            const bool write_prev = g == 0 && prev.L == kC;
+            if (write_prev) {
+                read(TM_DQ, out);
+                store_tile(out, m.dq, prev.t0, prev.j);
+            }
             product(1);  // T1 = K G^T
             add(TM_T1, TM_T1, fj, true);
             done(1);
+            if (write_prev) {
+                read(TM_DK, out);
+                store_tile(out, m.dk, prev.t0, prev.j);
+            }
             product(2);  // T1 = dv
-            uint32_t dv[16];
-            read(TM_T1, dv);
+            read(TM_T1, out);
             done(2);
-            write(dv, p.dv, im.t0, im.L, p.Hv, h);
+            if (im.L == kC) store_tile(out, m.dv, im.t0, h);
+            else write(out, p.dv, im.t0, im.L, p.Hv, h);
             product(3);  // T0 = dO V^T
             masked(true, l2, out);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                *reinterpret_cast<uint4 *>(sm + OFF_P + (cg >> 1) * kSub + sw128(row, 64 * (cg & 1) + 16 * x)) =
-                    make_uint4(out[4 * x], out[4 * x + 1], out[4 * x + 2], out[4 * x + 3]);
-            fence_proxy_async_smem();
+            if (write_prev || im.L == kC) clear_tile();
+            to_tile(out);
             done(3);
-            // here, not at product 0, where every later product of the head waits (4 % slower)
-            if (g == 0 && prev.L >= 0) write_item(prev);
+            if (g == 0 && prev.L >= 0 && !write_prev) write_item(prev);
             product(4);  // T1 = dO S
             add(TM_DQ, TM_T1, fi, g == 0);
             done(4);
@@ -409,7 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kEpiThreads / 32 + 1) {
         if (lane == 0) multiply(p, smem_u32(sm), ms, tmem, G);
     } else {
-        epilogue(p, sm, ms, tmem, G);
+        epilogue(maps, p, sm, ms, tmem, G);
+        if (tid == 0) bulk_wait_all();
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -423,7 +458,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 cudaError_t launch_backward(const BackwardPass &p, cudaStream_t s) {
     Maps m;
     if (!make_tile_map_bf16_128(&m.q, p.q, p.T, p.Hqk, kC) || !make_tile_map_bf16_128(&m.k, p.k, p.T, p.Hqk, kC) ||
-        !make_tile_map_bf16_128(&m.v, p.v, p.T, p.Hv, kC) || !make_tile_map_bf16_128(&m.g, p.dO, p.T, p.Hv, kC))
+        !make_tile_map_bf16_128(&m.v, p.v, p.T, p.Hv, kC) || !make_tile_map_bf16_128(&m.g, p.dO, p.T, p.Hv, kC) ||
+        !make_tile_map_bf16_128(&m.dq, p.dq, p.T, p.Hqk, kC) || !make_tile_map_bf16_128(&m.dk, p.dk, p.T, p.Hqk, kC) ||
+        !make_tile_map_bf16_128(&m.dv, p.dv, p.T, p.Hv, kC))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(gdn_linear_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmem);
