@@ -24,6 +24,10 @@
 // x from global memory to registers, a load's latency of 2,000 clocks a stage, 2.3.)
 // Bound: HBM (64 KB in, 32 KB image out per chunk and head, y shared by the
 // heads of a group through L2) against two or three products of 4.2 MFLOP.
+// Measured, 65,536 tokens of 48 heads in 144 segments: images 356 us, 5.2 TB/s of
+// 76 KB a chunk and head; sums 384 us, 2.2 us a chunk, where the conversion into three
+// parts, the products and the ring take turns at the limit (without the conversion's
+// arithmetic 18% less, without a third of the products 10%).
 #include "linear_tc.cuh"
 
 namespace gdn {
@@ -495,9 +499,10 @@ int device_sms() {
 
 // Segments, when one sequence could keep a CTA busy for much longer than an even
 // share of all chunks would (the segment sums walk the chunks a second time): as
-// long as the share, so that one wave of 148 CTAs has them all.  Measured with 48
-// heads and one sequence: 4,096 tokens 72 us with and 77 without, 65,536 tokens 550
-// and 800; segments for four waves 664.
+// long as the share, so that one wave of 148 CTAs has them all.  Measured with 48 heads and
+// one sequence, sums + scan + images against one segment: 4,096 tokens 31 + 6 + 33 us
+// and 81, 65,536 tokens 384 + 8 + 356 and 1,142.  Two passes at once, where the rule
+// says one segment: 57 + 10 + 54 and 59, 851 + 11 + 715 and 1,138.
 int64_t state_seg_chunks(int32_t N, int64_t T, int32_t H, int passes) {
     const int64_t longest = T / kC + 1, all = (T / kC + N) * H * passes, share = all / 148;
     if (N <= 0 || T <= 0 || longest <= 3 * share + 2) return 0;

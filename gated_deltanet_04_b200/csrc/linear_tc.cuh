@@ -129,8 +129,8 @@ __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, volati
     return true;
 }
 
-// One arrival for a warp whose lanes have done their part (and fenced it).  32
-// lanes arriving one by one are 32 atomics on one word: half a chunk's time.
+// One arrival for a warp whose lanes have done their part (and fenced it): 32
+// lanes arriving one by one would be 32 atomics on one word.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
