@@ -511,6 +511,35 @@ def test_repeatable_on_another_stream_and_in_a_graph():
             assert torch.equal(st, st2)
 
 
+def test_calls_in_a_row_share_a_workspace():
+    """A call's kernels may start before the ones ahead of them end; the next call's
+    must not touch a workspace, or inputs, that this one still reads."""
+    for shape, lens in [((1, 2, 128, 128, BF), [4096]), ((2, 6, 128, 128, BF), [700, 5, 900]),
+                        ((1, 2, 64, 64, F32), [1500, 40])]:
+        cs = [make(lens, *shape, seed=s) for s in (81, 82)]
+        want = [(run_prefill(c), run_backward(c)) for c in cs]
+        size = (len(lens), sum(lens), *shape[:4])
+        need = max(f(*size, dtype=shape[4]) for f in (gdn.gdn_linear_prefill_workspace_bytes,
+                                                      gdn.gdn_linear_prefill_backward_workspace_bytes))
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+        a = [[dev(c[x]) for x in ("q", "k", "v", "g", "s0", "cu", "do", "dsT")] for c in cs]
+        live = [torch.empty_like(x) for x in a[0]]
+        got = []
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for b in a:
+                for x, y in zip(live, b):
+                    x.copy_(y)
+                f = gdn.gdn_linear_prefill(*live[:6], scale=cs[0]["scale"], workspace=ws)
+                g = gdn.gdn_linear_prefill_backward(live[6], *live[:6], dfinal_state=live[7], scale=cs[0]["scale"],
+                                                    output_dinitial_state=True, workspace=ws)
+                got.append((f, g))
+        torch.cuda.synchronize()
+        for i, (f, g) in enumerate(got):
+            assert all(torch.equal(x, y) for x, y in zip(f, want[i % 2][0]))
+            assert all(torch.equal(x, y) for x, y in zip(g, want[i % 2][1]))
+
+
 def test_layer_run_norm_prefill_decode_and_gradients():
     """As a layer uses them: norm and rotation of a projection's queries and
     keys, linear prefill into states, decode steps, and the gradients of both."""
