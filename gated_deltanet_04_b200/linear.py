@@ -9,6 +9,10 @@ import torch
 from . import DTYPE, GdnError, _check, library
 
 F32, I32 = torch.float32, torch.int32
+# as torch.cuda.current_device() and torch.cuda.current_stream(i).cuda_stream give them
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _need(t, name, shape, dtype, dev):
@@ -28,10 +32,10 @@ def _run(dev, stream, call):
     """call(handle) with the tensors' device and the call's stream current, so that
     outputs and workspaces it allocates belong to that stream."""
     if stream is None:
-        if torch.cuda.current_device() == dev.index:
-            return call(torch.cuda.current_stream(dev).cuda_stream)
+        if _device() == dev.index:  # (the public calls build objects, 2 us of a call's 13)
+            return call(_raw_stream(dev.index))
         with torch.cuda.device(dev):
-            return call(torch.cuda.current_stream(dev).cuda_stream)
+            return call(_raw_stream(dev.index))
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, expected {dev}")
     with torch.cuda.device(dev), torch.cuda.stream(stream):
