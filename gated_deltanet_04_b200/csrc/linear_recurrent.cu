@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(kThreads)
 // One thread per four elements of a (sequence, head) state: walks the
 // sequence's segments in the pass's order, replacing each segment's sum by the
 // state that enters it.
+template <int kAhead>
 __global__ void gdn_linear_scan_kernel(const __grid_constant__ Pass p0, const __grid_constant__ Pass p1) {
     const Pass &p = blockIdx.z ? p1 : p0;
     next_may_start();
@@ -254,26 +255,29 @@ __global__ void gdn_linear_scan_kernel(const __grid_constant__ Pass p0, const __
     auto at = [&](int64_t j) {
         return reinterpret_cast<float4 *>(p.seg + ((base + seg(j)) * p.H + h) * (int64_t)per + x);
     };
-    // sums a few segments ahead of the chain, so that their loads overlap
-    constexpr int kAhead = 4;
+    // the sums of kAhead segments, and those of the next ones in flight meanwhile
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    float4 own[kAhead];
+    float4 own[kAhead], next[kAhead];
+    auto load = [&](int64_t j0) {  // (the last segment's sum is not there: nothing starts from it)
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) own[i] = i + 1 < count ? *at(i) : zero;
+        for (int i = 0; i < kAhead; ++i) next[i] = j0 + i + 1 < count ? *at(j0 + i) : zero;
+    };
+    load(0);
     for (int64_t j0 = 0; j0 < count; j0 += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) own[i] = next[i];
+        if (j0 + kAhead < count) load(j0 + kAhead);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int64_t j = j0 + i;
             if (j >= count) break;
-            const float4 sum = own[i];
-            own[i] = j + kAhead + 1 < count ? *at(j + kAhead) : zero;
             *at(j) = cur;
             const int64_t b = t0 + seg(j) * p.seg_len, e = b + p.seg_len < t1 ? b + p.seg_len : t1;
             const float f = expf(g * (float)(e - b));
-            cur.x = fmaf(f, cur.x, sum.x);
-            cur.y = fmaf(f, cur.y, sum.y);
-            cur.z = fmaf(f, cur.z, sum.z);
-            cur.w = fmaf(f, cur.w, sum.w);
+            cur.x = fmaf(f, cur.x, own[i].x);
+            cur.y = fmaf(f, cur.y, own[i].y);
+            cur.z = fmaf(f, cur.z, own[i].z);
+            cur.w = fmaf(f, cur.w, own[i].w);
         }
     }
 }
@@ -340,14 +344,19 @@ cudaError_t launch_scan(const Pass *passes, int count, cudaStream_t s) {
     if (units <= 0) return cudaSuccess;
     if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int per = p.Dc * p.Da / 4, threads = per < 256 ? per : 256;
-    return launch_after(gdn_linear_scan_kernel, true,
+    // the longest sequence's segments: with four at most (the tensor-core prefill of one
+    // sequence) fewer registers are in the way of the next kernel's start (4,096 tokens, 48
+    // heads: 106.5 us and 109.3); with many, more loads in flight (64 segments: 13 us and 21)
+    return launch_after(p.T <= 4 * p.seg_len ? gdn_linear_scan_kernel<4> : gdn_linear_scan_kernel<8>, true,
                         dim3((unsigned)units, (unsigned)((per + threads - 1) / threads), count), threads, 0, s, p,
                         passes[count - 1]);
 }
 
 // Enough segments for about eight of the 128-thread CTAs on each of 148 SMs,
-// none shorter than 64 tokens (a token is 0.17 us of latency in a pass; the two
-// other launches and a state's traffic cost about as much as 64 of them).
+// none shorter than 64 tokens, or 32 where a state is 64 x 64 or smaller: a token is
+// 0.17 us of latency in a pass, a segment costs its state's traffic and its step of the
+// scan.  (1,024 tokens, 4 heads: gradients at 64 x 64 84 us in segments of 32 and 103 of
+// 64, prefill at 128 x 128 48 and 43.)
 int64_t recurrent_seg_len(int32_t N, int64_t T, int32_t H, int32_t Da, int32_t Dc) {
     const int rows = Da == 16 ? 128 : 2 * kThreads / (Da / 16);
     const int64_t ctas = (int64_t)N * H * ((Dc + rows - 1) / rows);
@@ -355,7 +364,8 @@ int64_t recurrent_seg_len(int32_t N, int64_t T, int32_t H, int32_t Da, int32_t D
     const int64_t want = (148 * 8 + ctas - 1) / ctas;
     if (want <= 1) return 0;
     int64_t len = (T + want - 1) / want;
-    len = len < 64 ? 64 : (len + kTokBlock - 1) / kTokBlock * kTokBlock;
+    const int64_t least = Da * Dc > 64 * 64 ? 64 : 32;
+    len = len < least ? least : (len + kTokBlock - 1) / kTokBlock * kTokBlock;
     return len < T ? len : 0;
 }
 
