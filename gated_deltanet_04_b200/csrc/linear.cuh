@@ -27,6 +27,7 @@
 #include <utility>
 
 #include "gdn_internal.cuh"
+#include "sm100.cuh"
 
 namespace gdn {
 namespace linear {
@@ -150,6 +151,11 @@ struct Decay {
     template <bool kSlow>
     __device__ __forceinline__ float times(float x) const {
         return kSlow ? fmaf(f, x, x) : f * x;
+    }
+    template <bool kSlow>
+    __device__ __forceinline__ float2 times(float2 x) const {
+        const float2 f2 = make_float2(f, f);
+        return kSlow ? sm100::ffma2(f2, x, x) : sm100::fmul2(f2, x);
     }
 };
 

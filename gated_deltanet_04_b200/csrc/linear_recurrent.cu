@@ -10,10 +10,14 @@
 #include <type_traits>
 
 #include "linear.cuh"
+#include "sm100.cuh"
 
 namespace gdn {
 namespace linear {
 namespace {
+
+using sm100::ffma2;
+using sm100::fmul2;
 
 constexpr int kTokBlock = 16;
 constexpr int kThreads = 128;
@@ -65,8 +69,9 @@ __global__ void __launch_bounds__(kThreads)
     if (kOut && st < 0 && tid == 0 && rb == 0 && h == 0) raise_error(p.err, GDN_ERR_BAD_SLOT);
     const int64_t st_off = (st * p.H + h) * (int64_t)p.Dc * DA;
 
-    // column m*4*LPR + 4*l + e of row rows[r]
-    float M[RPT][16];
+    // columns m*4*LPR + 4*l + (0, 1), (2, 3) of row rows[r]: pairs, for two multiply-adds an
+    // instruction
+    float2 M[RPT][8];
     const bool from_seg = kOut && p.seg && sp.count > 1;
     const bool from_m0 = kOut && !from_seg && p.m0 && st >= 0 && !state_fresh(p.map, sp.n);
     const float *src = from_seg ? p.seg + seg_off : from_m0 ? p.m0 + st_off : nullptr;
@@ -84,7 +89,8 @@ __global__ void __launch_bounds__(kThreads)
                 else
                     v = *reinterpret_cast<const float4 *>(src + (int64_t)i * DA + d);
             }
-            M[r][4 * m] = v.x; M[r][4 * m + 1] = v.y; M[r][4 * m + 2] = v.z; M[r][4 * m + 3] = v.w;
+            M[r][2 * m] = make_float2(v.x, v.y);
+            M[r][2 * m + 1] = make_float2(v.z, v.w);
         }
     const Decay decay(p.log_decay[h]);
     const int64_t len = sp.t1 - sp.t0;
@@ -143,31 +149,34 @@ __global__ void __launch_bounds__(kThreads)
             constexpr bool kSlow = decltype(slow)::value;
             // one token: the read-outs' partial sums of this lane's columns
             auto token_step = [&](int tt, float (&acc)[RPT]) {
-                float cv[RPT], part[RPT][4];
+                float2 cv[RPT], part[RPT][4];
 #pragma unroll
-                for (int r = 0; r < RPT; ++r) cv[r] = cs[tt][rows[r]];
+                for (int r = 0; r < RPT; ++r) cv[r] = make_float2(cs[tt][rows[r]], cs[tt][rows[r]]);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const float4 b4 = *reinterpret_cast<const float4 *>(&bs[tt][m * 4 * LPR + 4 * l]);
                     float4 a4;
                     if (kOut) a4 = *reinterpret_cast<const float4 *>(&as_[tt][m * 4 * LPR + 4 * l]);
-                    const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
-                    const float av[4] = {a4.x, a4.y, a4.z, a4.w};
+                    const float2 bv[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
+                    const float2 av[2] = {make_float2(a4.x, a4.y), make_float2(a4.z, a4.w)};
 #pragma unroll
                     for (int r = 0; r < RPT; ++r) {
-                        part[r][m] = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float &x = M[r][4 * m + e];
+                        for (int e = 0; e < 2; ++e) {
+                            float2 &x = M[r][2 * m + e];
                             if (!kRev) x = decay.times<kSlow>(x);
-                            x = fmaf(cv[r], bv[e], x);
-                            if (kOut) part[r][m] = fmaf(x, av[e], part[r][m]);
+                            x = ffma2(cv[r], bv[e], x);
+                            if (kOut) part[r][m] = e ? ffma2(x, av[e], part[r][m]) : fmul2(x, av[e]);
                             if (kRev) x = decay.times<kSlow>(x);
                         }
                     }
                 }
+                if (kOut) {
 #pragma unroll
-                for (int r = 0; r < RPT; ++r) acc[r] = (part[r][0] + part[r][1]) + (part[r][2] + part[r][3]);
+                    for (int r = 0; r < RPT; ++r)
+                        acc[r] = ((part[r][0].x + part[r][0].y) + (part[r][1].x + part[r][1].y)) +
+                                 ((part[r][2].x + part[r][2].y) + (part[r][3].x + part[r][3].y));
+                }
             };
             // sums over the row's lanes, staged by the first of them
             auto finish = [&](int tt, float (&acc)[RPT]) {
@@ -216,7 +225,7 @@ __global__ void __launch_bounds__(kThreads)
                 const int i = row0 + rows[r], d = m * 4 * LPR + 4 * l;
                 if (i < p.Dc)
                     *reinterpret_cast<float4 *>(dst + (int64_t)i * DA + d) =
-                        make_float4(M[r][4 * m], M[r][4 * m + 1], M[r][4 * m + 2], M[r][4 * m + 3]);
+                        make_float4(M[r][2 * m].x, M[r][2 * m].y, M[r][2 * m + 1].x, M[r][2 * m + 1].y);
             }
     }
 }
