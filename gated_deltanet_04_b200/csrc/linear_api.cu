@@ -59,17 +59,19 @@ size_t seg_bytes(const Call &c, int64_t seg_len) {
     return seg_len ? al256((size_t)gdn::linear::slots_of(c.T, c.N, seg_len) * c.Hv * c.Dk * c.Dv * 4) : 0;
 }
 
-// The tensor-core kernels serve 128-wide bf16 heads, from 16 tokens a sequence on
-// average: below that a token at a time is faster than 128-token chunks.  (48 heads:
-// 64 sequences of 16 tokens 326 us a token at a time and 318 on tensor cores, 4
-// sequences of 3 on average 11 and 32.)
-bool tensor_cores(const Call &c) {
-    return c.dt == GDN_DTYPE_BF16 && c.Dk == 128 && c.Dv == 128 && c.T > (int64_t)16 * c.N;
+// The tensor-core kernels serve 128-wide bf16 heads, from `least` tokens a sequence on
+// average: below that a token at a time is faster than 128-token chunks.  (48 heads, a
+// token at a time and on tensor cores: prefill of 64 sequences of 16 tokens 293 and 308
+// us, of 24 393 and 307, of 8 sequences of 12 32 and 46; gradients of 64 sequences of 4
+// tokens 638 and 601, of 8 98 and 85, of one 41 and 34.)
+constexpr int kLeastPrefill = 16, kLeastBackward = 2;
+bool tensor_cores(const Call &c, int least) {
+    return c.dt == GDN_DTYPE_BF16 && c.Dk == 128 && c.Dv == 128 && c.T > (int64_t)least * c.N;
 }
 
 size_t prefill_bytes(const Call &c) {
     if (check(c) != GDN_OK || check_size(c) != GDN_OK || c.T == 0) return 0;
-    if (tensor_cores(c))
+    if (tensor_cores(c, kLeastPrefill))
         return gdn::linear::state_dump_bytes(c.N, c.T, c.Hv) + gdn::linear::state_seg_bytes(c.N, c.T, c.Hv, 1);
     return seg_bytes(c, gdn::linear::recurrent_seg_len(c.N, c.T, c.Hv, c.Dk, c.Dv));
 }
@@ -79,7 +81,7 @@ size_t prefill_bytes(const Call &c) {
 // summed from fp32 partials.
 size_t backward_bytes(const Call &c) {
     if (check(c) != GDN_OK || check_size(c) != GDN_OK || c.T == 0) return 0;
-    if (tensor_cores(c))
+    if (tensor_cores(c, kLeastBackward))
         return 2 * gdn::linear::state_dump_bytes(c.N, c.T, c.Hv) + 2 * gdn::linear::state_seg_bytes(c.N, c.T, c.Hv, 2);
     const size_t a = seg_bytes(c, gdn::linear::recurrent_seg_len(c.N, c.T, c.Hv, c.Dk, c.Dv));
     const size_t b = seg_bytes(c, gdn::linear::recurrent_seg_len(c.N, c.T, c.Hv, c.Dv, c.Dk));
@@ -123,7 +125,7 @@ gdn_status prefill(const void *q, const void *k, const void *v, const float *log
     const size_t need = prefill_bytes(c);
     if (need > 0 && (ws == nullptr || ws_bytes < need)) return GDN_ERR_INVALID_ARGUMENT;
     if (c.N == 0 || (c.T == 0 && sT == nullptr)) return GDN_OK;  // nothing observable to do
-    if (tensor_cores(c)) {
+    if (tensor_cores(c, kLeastPrefill)) {
         gdn::linear::StatePass st = states(c, v, k, c.Hqk, log_decay, 1.f, false, s0, sT, ws, 0, 1, err);
         st.map = map;
         const cudaError_t e = gdn::linear::launch_states(&st, 1, s);
@@ -226,7 +228,7 @@ gdn_status gdn_linear_prefill_backward(const void *dO, const void *q, const void
     if (N == 0 || (T == 0 && dinitial_state == nullptr)) return GDN_OK;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (tensor_cores(c)) {
+    if (tensor_cores(c, kLeastBackward)) {
         // S and G do not depend on one another: one launch for both
         const gdn::linear::StatePass sg[2] = {states(c, v, k, Hqk, log_decay, 1.f, false, initial_state, nullptr,
                                                      workspace, 0, 2, dev_error_flag),

@@ -544,12 +544,12 @@ GDN_API size_t gdn_prefill_host_scratch_bytes(int64_t T, int32_t Hqk, int32_t Hv
  * dtype; T < 2^31 and (T / 128 + N) * Hv < 2^29, else GDN_ERR_UNSUPPORTED.
  *
  * Kernels: with bf16 I/O, Dk = Dv = 128 and more than 16 tokens a sequence on
- * average, chunks of 128 tokens on tensor cores (tcgen05); their operands are bf16
- * (the masked scores and the states entering a chunk are rounded to it, 2^-8 of a
- * term), the fp32 states keep fp32 accuracy.  Everything else runs a token at a
- * time in fp32 on CUDA cores.  A value that is not finite spreads as the sums
- * have it, and on tensor cores also to earlier tokens of its own 128-token chunk
- * and head; never to another sequence.
+ * average (the gradients: 2), chunks of 128 tokens on tensor cores (tcgen05);
+ * their operands are bf16 (the masked scores and the states entering a chunk are
+ * rounded to it, 2^-8 of a term), the fp32 states keep fp32 accuracy.  Everything
+ * else runs a token at a time in fp32 on CUDA cores.  A value that is not finite
+ * spreads as the sums have it, and on tensor cores also to earlier tokens of its
+ * own 128-token chunk and head; never to another sequence.
  */
 
 /*

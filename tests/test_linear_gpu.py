@@ -244,6 +244,12 @@ def test_backward_segments_and_groups():
         check_backward(c, run_backward(c))
 
 
+@pytest.mark.parametrize("lens", [[2], [3], [4, 3, 0, 5], [9, 1] * 12], ids=str)
+def test_backward_of_short_sequences(lens):
+    c = make(lens, 2, 6, 128, 128, BF, seed=33 + sum(lens))
+    check_backward(c, run_backward(c))
+
+
 def test_backward_without_states_and_in_place():
     for shape in [(2, 4, 32, 64, F32), (1, 3, 128, 128, BF)]:
         c = make([513], *shape, seed=31)
