@@ -88,9 +88,10 @@ cudaError_t launch_after(void (*kernel)(P...), bool after, dim3 grid, int thread
     return cudaGetLastError();
 }
 
-// First slot of sequence n among slots of `len` tokens.
+// First slot of sequence n among slots of `len` tokens.  (A 32-bit division, which is a
+// fraction of a 64-bit one: len <= 2^31, and a negative entry of cu is found elsewhere.)
 __device__ __forceinline__ int64_t slot_base(const int32_t *cu, int n, int64_t len) {
-    return (cu ? (int64_t)cu[n] / len : 0) + n;
+    return (int64_t)(cu ? (uint32_t)cu[n] / (uint32_t)len : 0u) + n;
 }
 
 // One segment (or chunk): tokens [t0, t1) of sequence n, number `s` of `count`.
@@ -113,8 +114,9 @@ __device__ __forceinline__ bool find_span(const int32_t *cu, int32_t N, int64_t 
     int64_t b, e;
     if (!seq_range(cu, lo, N, T, err, b, e)) return false;
     sp.n = lo;
-    sp.s = slot - (b / len + lo);
-    sp.count = e > b ? (e - b + len - 1) / len : 1;
+    // 0 <= b <= e <= T < 2^31
+    sp.s = slot - ((int64_t)((uint32_t)b / (uint32_t)len) + lo);
+    sp.count = e > b ? (int64_t)((uint32_t)(e - b - 1) / (uint32_t)len) + 1 : 1;
     if (sp.s < 0 || sp.s >= sp.count) return false;
     sp.t0 = b + sp.s * len;
     sp.t1 = sp.t0 + len < e ? sp.t0 + len : e;

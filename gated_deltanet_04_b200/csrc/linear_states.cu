@@ -42,6 +42,8 @@ constexpr int kStateWarps = 8, kConvWarps = 16, kGroup = 8;  // warps; warps per
 constexpr int kStateThreads = kStateWarps * 32, kConvThreads = kConvWarps * 32;
 constexpr int kThreads = kStateThreads + kConvThreads + 64;
 constexpr uint32_t kStage = 2 * kPart;       // x, y
+constexpr uint32_t kStateRow = 4 * kD + 16;  // a row of the fp32 state, staged in the ring
+static_assert(kD * kStateRow <= kRing * kStage, "the state in the ring");
 constexpr uint32_t OFF_IMAGE = kRing * kStage;
 constexpr uint32_t OFF_MISC = OFF_IMAGE + kTile;
 
@@ -452,22 +454,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float *dst = kDump ? (last && p.mT && st >= 0 ? p.mT + (st * p.H + h) * (int64_t)(kD * kD) : nullptr)
                            : p.seg + (slot * p.H + h) * (int64_t)(kD * kD);
-        if (ok && dst) {
+        // through the ring, which is free now: its rows 16 bytes apart in the banks, each a
+        // bulk copy (rows straight from registers are a line per thread: 4,200 clocks)
+        if (dst) {
+            float *stage = reinterpret_cast<float *>(sm + row * kStateRow) + 64 * half;
 #pragma unroll
             for (int c = 0; c < 64; c += 32) {
                 float v[32];
                 tmem_ld32(trow + TM_S + c, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int x = 0; x < 32; x += 8) {
-                    uint32_t u[8];
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) u[y] = __float_as_uint(v[x + y]);
-                    store_b256(dst + at + c + x, u);
-                }
+                for (int x = 0; x < 32; x += 4)
+                    *reinterpret_cast<float4 *>(stage + c + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+            }
+            fence_proxy_async_smem();
+            state_barrier();
+            if (ok && tid < kD) {
+                bulk_store(dst + tid * kD, sm + tid * kStateRow, kD * sizeof(float));
+                bulk_commit();
             }
         }
-        if (kDump && tid == 0) bulk_wait_all();
+        if (tid < kD) bulk_wait_all();
     }
     __syncwarp();
     tc_fence_before_sync();
