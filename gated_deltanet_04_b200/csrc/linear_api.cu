@@ -61,9 +61,9 @@ size_t seg_bytes(const Call &c, int64_t seg_len) {
 
 // The tensor-core kernels serve 128-wide bf16 heads, from `least` tokens a sequence on
 // average: below that a token at a time is faster than 128-token chunks.  (48 heads, a
-// token at a time and on tensor cores: prefill of 64 sequences of 16 tokens 293 and 308
-// us, of 24 393 and 307, of 8 sequences of 12 32 and 46; gradients of 64 sequences of 4
-// tokens 638 and 601, of 8 98 and 85, of one 41 and 34.)
+// token at a time and on tensor cores: prefill of 64 sequences of 16 tokens 293 and 290
+// us, of 24 393 and 291, of 8 sequences of 12 32 and 44; gradients of 64 sequences of 4
+// tokens 638 and 570, of 8 98 and 81, of one 41 and 33.)
 constexpr int kLeastPrefill = 16, kLeastBackward = 2;
 bool tensor_cores(const Call &c, int least) {
     return c.dt == GDN_DTYPE_BF16 && c.Dk == 128 && c.Dv == 128 && c.T > (int64_t)least * c.N;
