@@ -74,7 +74,7 @@ __device__ void produce(const Maps &m, const BackwardPass &p, int64_t items, uin
     uint32_t cnt[kBufs] = {0, 0, 0, 0, 0, 0};  // loads issued into each buffer
     bool ok = true;
     auto acquire = [&](int b) {
-        if (ok && cnt[b] > 0) ok = role_wait(&ms->empty[b], (cnt[b] - 1) & 1, abort, p.err);
+        if (ok && cnt[b] > 0) ok = thread_wait(&ms->empty[b], (cnt[b] - 1) & 1, abort, p.err);
         if (ok) {
             ++cnt[b];
             mbar_arrive_expect_tx(&ms->full[b], kTile);
@@ -87,7 +87,7 @@ __device__ void produce(const Maps &m, const BackwardPass &p, int64_t items, uin
         const int j = (int)(it - slot * p.Hqk);
         Span sp;
         if (!find_span(p.cu, p.N, p.T, kC, slot, p.err, sp) || sp.t1 <= sp.t0) continue;
-        if (n >= 2 && !(ok = role_wait(&ms->item_empty[n & 1], ((n >> 1) - 1) & 1, abort, p.err))) break;
+        if (n >= 2 && !(ok = thread_wait(&ms->item_empty[n & 1], ((n >> 1) - 1) & 1, abort, p.err))) break;
         ms->item[n & 1] = {sp.t0, (int32_t)(sp.t1 - sp.t0), j};
         mbar_arrive(&ms->item_full[n & 1]);
         ++n;
@@ -110,7 +110,7 @@ __device__ void produce(const Maps &m, const BackwardPass &p, int64_t items, uin
             load_tile(sm + B_V * kTile, &m.v, &ms->full[B_V], h, sp.t0);
         }
     }
-    if (ok && n >= 2) ok = role_wait(&ms->item_empty[n & 1], ((n >> 1) - 1) & 1, abort, p.err);
+    if (ok && n >= 2) ok = thread_wait(&ms->item_empty[n & 1], ((n >> 1) - 1) & 1, abort, p.err);
     if (ok) {
         ms->item[n & 1].L = -1;
         mbar_arrive(&ms->item_full[n & 1]);
@@ -126,7 +126,7 @@ __device__ void produce(const Maps &m, const BackwardPass &p, int64_t items, uin
 // each, because two products may be done before the first is waited for.
 __device__ void multiply(const BackwardPass &p, uint32_t sbase, Misc *ms, uint32_t tmem, int G) {
     volatile int32_t *abort = &ms->abort;
-    auto wait = [&](uint64_t &bar, uint32_t parity) { return role_wait(&bar, parity & 1, abort, p.err); };
+    auto wait = [&](uint64_t &bar, uint32_t parity) { return thread_wait(&bar, parity & 1, abort, p.err); };
     auto tile = [&](int b) { return sbase + b * kTile; };
     const uint32_t dq = tmem + TM_DQ, dk = tmem + TM_DK, T0 = tmem + TM_T0, T1 = tmem + TM_T1;
     const uint32_t P = sbase + OFF_P;
@@ -213,7 +213,7 @@ __device__ void epilogue(const Maps &m, const BackwardPass &p, uint8_t *sm, Misc
     const int row = quad * 32 + lane;  // token of the chunk; columns 32 cg ..
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16), tcol = trow + 32 * cg;
     const float *up = nullptr;
-    auto wait = [&](uint64_t &bar, uint32_t parity) { return role_wait(&bar, parity & 1, abort, p.err); };
+    auto wait = [&](uint64_t &bar, uint32_t parity) { return warp_wait(&bar, parity & 1, abort, p.err); };
     // After a wait given up the remaining ones fail at once (abort is up), and a
     // thread goes on through its barriers: they stay whole.
     bool ok = true;

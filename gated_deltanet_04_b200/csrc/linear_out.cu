@@ -51,9 +51,9 @@ __device__ void produce(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const 
                         int64_t items, uint8_t *sm, Misc *ms, int G) {
     uint32_t n = 0, r = 0;  // items and ring tiles so far
     volatile int32_t *abort = &ms->abort;
-    auto wait_q = [&]() { return n < 2 || role_wait(&ms->empty_q[n & 1], ((n >> 1) - 1) & 1, abort, p.err); };
+    auto wait_q = [&]() { return n < 2 || thread_wait(&ms->empty_q[n & 1], ((n >> 1) - 1) & 1, abort, p.err); };
     auto wait_ring = [&]() {
-        return r < kRing || role_wait(&ms->empty_v[r % kRing], (r / kRing - 1) & 1, abort, p.err);
+        return r < kRing || thread_wait(&ms->empty_v[r % kRing], (r / kRing - 1) & 1, abort, p.err);
     };
     bool ok = true, k_issued = true;
     for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
@@ -65,7 +65,7 @@ __device__ void produce(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const 
         ms->item[n & 1] = {sp.t0, (int32_t)(sp.t1 - sp.t0), j};
         mbar_arrive_expect_tx(&ms->full_q[n & 1], kTile);
         load_tile(sm + OFF_Q + (n & 1) * kTile, &tm_q, &ms->full_q[n & 1], j, sp.t0);
-        k_issued = ok = n < 1 || role_wait(&ms->empty_k, (n - 1) & 1, abort, p.err);
+        k_issued = ok = n < 1 || thread_wait(&ms->empty_k, (n - 1) & 1, abort, p.err);
         ++n;
         if (!ok) break;
         mbar_arrive_expect_tx(&ms->full_k, kTile);
@@ -100,7 +100,7 @@ __device__ void produce(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const 
 __device__ void multiply(const OutPass &p, uint32_t sbase, Misc *ms, uint32_t tmem, int G) {
     volatile int32_t *abort = &ms->abort;
     uint32_t u = 0, r = 0;  // v-heads and ring tiles so far
-    auto wait = [&](uint64_t &bar, uint32_t parity) { return role_wait(&bar, parity & 1, abort, p.err); };
+    auto wait = [&](uint64_t &bar, uint32_t parity) { return thread_wait(&bar, parity & 1, abort, p.err); };
     for (uint32_t n = 0;; ++n) {
         if (!wait(ms->full_q[n & 1], n >> 1)) break;
         if (ms->item[n & 1].L < 0) return;
@@ -139,7 +139,7 @@ __device__ void epilogue(const OutPass &p, uint8_t *sm, Misc *ms, uint32_t tmem,
     const int i = quad * 32 + lane;  // token of the chunk; its columns 64 half ..
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
     float *pow = ms->pow[warp];
-    auto wait = [&](uint64_t &bar, uint32_t parity) { return role_wait(&bar, parity & 1, abort, p.err); };
+    auto wait = [&](uint64_t &bar, uint32_t parity) { return warp_wait(&bar, parity & 1, abort, p.err); };
 
     // P of v-head number u: Q K^T times scale lam^{i-j}, j <= i
     auto make_p = [&](uint32_t u, float l2) {

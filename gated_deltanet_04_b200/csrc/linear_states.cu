@@ -87,7 +87,7 @@ __device__ void produce(const CUtensorMap &tm_x, const CUtensorMap &tm_y, const 
         const int L = w.length(it);
         for (int j0 = 0; j0 < L; j0 += kRows, ++r) {
             const int b = r % kRing;
-            if (r >= kRing && !role_wait(&ms->raw_empty[b], (r / kRing - 1) & 1, &ms->abort, err)) {
+            if (r >= kRing && !thread_wait(&ms->raw_empty[b], (r / kRing - 1) & 1, &ms->abort, err)) {
                 // given up: let the loads in flight land before the CTA ends
                 for (uint32_t x = r - kRing; x < r; ++x)
                     mbar_wait_bounded(&ms->raw_full[x % kRing], (x / kRing) & 1, kWaitLimit);
@@ -173,7 +173,7 @@ __device__ void convert(const Walk &w, uint8_t *sm, Misc *ms, uint32_t tlane, in
         const uint32_t(*wt)[kC / 2] = ms->weight[L < kC];
         const float2 *w32 = ms->weight32[L < kC];
         const int at = a.s * (kRows / 2) + 16 * half;
-        if (!role_wait(&ms->raw_full[b], (r / kRing) & 1, &ms->abort, err)) return;
+        if (!warp_wait(&ms->raw_full[b], (r / kRing) & 1, &ms->abort, err)) return;
         const uint8_t *x = sm + b * kStage;
         uint32_t in[16];
 #pragma unroll
@@ -220,7 +220,7 @@ __device__ void convert(const Walk &w, uint8_t *sm, Misc *ms, uint32_t tlane, in
                 }
             }
             // as late as can be: the MMAs of the other group's stage cover what follows
-            if (q0 == 0 && r >= 2 && !role_wait(&ms->part_empty[group], ((r >> 1) - 1) & 1, &ms->abort, err)) return;
+            if (q0 == 0 && r >= 2 && !warp_wait(&ms->part_empty[group], ((r >> 1) - 1) & 1, &ms->abort, err)) return;
             tc_fence_after_sync();
             tmem_st8u(dst + q0, hi);
             tmem_st8u(dst + 32 + q0, mid);
@@ -236,7 +236,7 @@ __device__ void convert(const Walk &w, uint8_t *sm, Misc *ms, uint32_t tlane, in
         tc_fence_before_sync();
         warp_arrive(&ms->part_full[group]);
         if (kParts == 3) {
-            if (!role_wait(&ms->first_empty[group], (r >> 1) & 1, &ms->abort, err)) return;
+            if (!warp_wait(&ms->first_empty[group], (r >> 1) & 1, &ms->abort, err)) return;
             tc_fence_after_sync();
             tmem_st16u(dst, lo);
             tmem_wait_st();
@@ -257,13 +257,13 @@ __device__ void multiply(const Walk &w, uint32_t sbase, uint32_t tmem, Misc *ms,
         const int L = w.length(it);
         const int sum = it % kSums;
         const uint32_t d = tmem + TM_SUM + 128 * sum;
-        if (it >= kSums && !(ok = role_wait(&ms->sum_empty[sum], (it / kSums - 1) & 1, &ms->abort, err))) break;
+        if (it >= kSums && !(ok = thread_wait(&ms->sum_empty[sum], (it / kSums - 1) & 1, &ms->abort, err))) break;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             if (s * kRows >= L) break;
             const uint32_t buf = r & 1;
-            if (!(ok = role_wait(&ms->raw_full[b], lap & 1, &ms->abort, err) &&
-                       role_wait(&ms->part_full[buf], (r >> 1) & 1, &ms->abort, err)))
+            if (!(ok = thread_wait(&ms->raw_full[b], lap & 1, &ms->abort, err) &&
+                       thread_wait(&ms->part_full[buf], (r >> 1) & 1, &ms->abort, err)))
                 break;
             tc_fence_after_sync();
             const uint64_t y = y0 + b * (kStage >> 4);
@@ -277,7 +277,7 @@ __device__ void multiply(const Walk &w, uint32_t sbase, uint32_t tmem, Misc *ms,
             if (kParts == 3) mma_commit(&ms->first_empty[buf]);
             part(x + 32, false);
             if (kParts == 3) {
-                if (!(ok = role_wait(&ms->third_full[buf], (r >> 1) & 1, &ms->abort, err))) break;
+                if (!(ok = thread_wait(&ms->third_full[buf], (r >> 1) & 1, &ms->abort, err))) break;
                 tc_fence_after_sync();
                 part(x, false);
             }
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int it = 0; it < w.nch; ++it) {
             // every warp goes on after a wait given up, so that the barriers stay whole
             const int sum = it % kSums;
-            if (ok) ok = role_wait(&ms->sum_full[sum], (it / kSums) & 1, &ms->abort, p.err);
+            if (ok) ok = warp_wait(&ms->sum_full[sum], (it / kSums) & 1, &ms->abort, p.err);
             tc_fence_after_sync();
             const bool more = kDump && it + 1 < w.nch;
             if (more) {

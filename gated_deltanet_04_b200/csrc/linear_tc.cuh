@@ -113,9 +113,11 @@ __device__ __forceinline__ void load_tile(void *dst, const CUtensorMap *map, uin
 
 // Waits of the warp-specialised kernels: give up when another role has
 // (`abort`), or after kWaitLimit clocks, raising `abort` and the error flag.
+// thread_wait is for the roles of one thread; the lanes of a warp may get different
+// answers from it (the barrier completes for one as `abort` goes up for another).
 // (A suspend-time hint on the wait made the whole chunk-state kernel 10% slower:
 // the hardware wakes such a warp later.)
-__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, volatile int32_t *abort, int32_t *err) {
+__device__ __forceinline__ bool thread_wait(uint64_t *bar, uint32_t parity, volatile int32_t *abort, int32_t *err) {
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (!mbar_try_wait(bar, parity)) {
@@ -127,6 +129,11 @@ __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, volati
         }
     }
     return true;
+}
+// The same for the roles of whole warps: one answer for all 32 lanes, so that none leaves
+// while others go on to an instruction that needs all of them.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int32_t *abort, int32_t *err) {
+    return __all_sync(0xffffffffu, thread_wait(bar, parity, abort, err));
 }
 
 // One arrival for a warp whose lanes have done their part (and fenced it): 32
