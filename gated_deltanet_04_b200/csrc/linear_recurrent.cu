@@ -7,8 +7,6 @@
 // read-out) and one shuffle reduction of the read-out.  Token inputs come
 // through shared memory, kTokBlock at a time, the next block's loads in flight
 // while one is computed.
-#include <type_traits>
-
 #include "linear.cuh"
 #include "sm100.cuh"
 
@@ -248,6 +246,7 @@ __global__ void gdn_linear_scan_kernel(const __grid_constant__ Pass p0, const __
     if (count == 1) return;  // the pass itself starts from the entering state
     const int64_t base = slot_base(p.cu, n, p.seg_len);
     const float g = p.log_decay[h];
+    const Decay whole(g * (float)p.seg_len), tail(g * (float)(t1 - t0 - (count - 1) * p.seg_len));
     float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
     const int64_t st = state_index(p.map, n);
     if (p.m0 && st >= 0 && !state_fresh(p.map, n)) {
@@ -281,12 +280,15 @@ __global__ void gdn_linear_scan_kernel(const __grid_constant__ Pass p0, const __
             const int64_t j = j0 + i;
             if (j >= count) break;
             *at(j) = cur;
-            const int64_t b = t0 + seg(j) * p.seg_len, e = b + p.seg_len < t1 ? b + p.seg_len : t1;
-            const float f = expf(g * (float)(e - b));
-            cur.x = fmaf(f, cur.x, own[i].x);
-            cur.y = fmaf(f, cur.y, own[i].y);
-            cur.z = fmaf(f, cur.z, own[i].z);
-            cur.w = fmaf(f, cur.w, own[i].w);
+            const Decay d = seg(j) == count - 1 ? tail : whole;
+            auto add = [&](auto slow) {
+                constexpr bool kSlow = decltype(slow)::value;
+                const float2 lo = d.plus<kSlow>(make_float2(cur.x, cur.y), make_float2(own[i].x, own[i].y));
+                const float2 hi = d.plus<kSlow>(make_float2(cur.z, cur.w), make_float2(own[i].z, own[i].w));
+                cur = make_float4(lo.x, lo.y, hi.x, hi.y);
+            };
+            if (d.slow) add(std::true_type{});
+            else add(std::false_type{});
         }
     }
 }

@@ -4,7 +4,7 @@
 // tensor memory; each chunk's sum of outer products is one fresh tensor-core
 // accumulator added to it by fp32 FMAs (the tensor core's own accumulation over
 // thousands of chunks would truncate, and with a slow decay the loss would add
-// up).
+// up; for the same reason a slow decay acts by expm1, see Decay).
 //
 // Precision: y enters as it is (bf16); x times its decay weight is split into
 // bf16 parts, hi + mid + lo, which together keep fp32's 24 bits: three MMA
@@ -420,7 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_wait_st();
         if (kDump && w.nch > 0) store_image(0);
-        const float dec_full = exp2f(l2 * (float)kC);
+        const float g = p.log_decay[h];
+        const Decay full(g * (float)kC);  // a product of its own, once per chunk: see Decay
         bool ok = true;
         for (int it = 0; it < w.nch; ++it) {
             // every warp goes on after a wait given up, so that the barriers stay whole
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 state_barrier();
             }
             const int L = w.length(it);
-            const float dec = L < kC ? exp2f(l2 * (float)L) : dec_full;
+            const Decay dec = L < kC ? Decay(g * (float)L) : full;
 #pragma unroll
             for (int c = 0; c < 64; c += 16) {
                 float v[16], d[16];
@@ -444,8 +445,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_before_sync();
                     warp_arrive(&ms->sum_empty[sum]);
                 }
+                auto add = [&](auto slow) {  // a uniform choice
 #pragma unroll
-                for (int x = 0; x < 16; ++x) v[x] = fmaf(dec, v[x], d[x]);
+                    for (int x = 0; x < 16; x += 2) {
+                        const float2 s = dec.plus<decltype(slow)::value>(make_float2(v[x], v[x + 1]),
+                                                                         make_float2(d[x], d[x + 1]));
+                        v[x] = s.x;
+                        v[x + 1] = s.y;
+                    }
+                };
+                if (dec.slow) add(std::true_type{});
+                else add(std::false_type{});
                 tmem_st16(trow + TM_S + c, v);
                 if (more) draw(c, v);
             }
