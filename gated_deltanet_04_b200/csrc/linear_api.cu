@@ -35,9 +35,8 @@ gdn_status check(const Call &c) {
 gdn_status check_size(const Call &c) {
     if (!supported_dim(c.Dk) || !supported_dim(c.Dv)) return GDN_ERR_UNSUPPORTED;
     // token indices are 32-bit in cu_seqlens and in TMA coordinates, and the
-    // largest grid has (T / 128 + N) * Hv * 4 CTAs
-    if (c.T > 0x7fffffffLL || (c.T / 128 + c.N) * (int64_t)c.Hv * 4 > 0x7fffffffLL)
-        return GDN_ERR_UNSUPPORTED;
+    // largest grid has (T / 128 + N + 1) * Hv * 4 CTAs (divided: the product can pass 64 bits)
+    if (c.T > 0x7fffffffLL || c.T / 128 + c.N + 1 > 0x7fffffffLL / 4 / c.Hv) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 
@@ -285,8 +284,9 @@ gdn_status decode(const void *q, const void *k, const void *v, gdn_dtype io_dtyp
     const void *ins[] = {q, k, v, log_decay};
     const void *outs[] = {o, state};
     if (gdn_status e = check_pointers(all, ins, outs)) return e;
-    if (!supported_dim(Dk)) return GDN_ERR_UNSUPPORTED;
-    if ((int64_t)N * Hv > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    if (!supported_dim(Dk) || Dv > 1 << 30) return GDN_ERR_UNSUPPORTED;
+    // a grid of one CTA per (sequence, v-head), or per 128 state rows of it where Dk = 128
+    if ((int64_t)N * Hv > 0x7fffffffLL / (Dk == 128 ? (Dv + 127) / 128 : 1)) return GDN_ERR_UNSUPPORTED;
     if (N == 0) return GDN_OK;
     return from_cuda(gdn::linear::launch_decode({q, k, v, o, io_dtype, log_decay, scale, state, map, N, Hqk,
                                                  Hv, Dk, Dv, err},

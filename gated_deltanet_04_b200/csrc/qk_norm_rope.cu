@@ -478,10 +478,12 @@ gdn_status common(RopeArgs &a, const void *xq, const void *xk, gdn_dtype dt, int
     }
     const int64_t esz = dt == GDN_DTYPE_BF16 ? 2 : 4;
     if (xq_stride < (int64_t)Hq * D || (Hk > 0 && xk_stride < (int64_t)Hk * D)) return GDN_ERR_INVALID_ARGUMENT;
-    if ((xq_stride * esz) % 16 || (Hk > 0 && (xk_stride * esz) % 16)) return GDN_ERR_INVALID_ARGUMENT;
-    if (!supported(D) || rot % 16 != 0 || Hq > 32768 - Hk) return GDN_ERR_UNSUPPORTED;
     // a token's bytes are 32-bit in the kernels
     if (xq_stride > 0x3fffffff || (Hk > 0 && xk_stride > 0x3fffffff)) return GDN_ERR_UNSUPPORTED;
+    if ((xq_stride * esz) % 16 || (Hk > 0 && (xk_stride * esz) % 16)) return GDN_ERR_INVALID_ARGUMENT;
+    if (!supported(D) || rot % 16 != 0 || Hq > 32768 - Hk) return GDN_ERR_UNSUPPORTED;
+    // the grid's x dimension (divided: the product can pass 64 bits)
+    if (T > ((int64_t)1 << 33) / (Hq + Hk)) return GDN_ERR_UNSUPPORTED;
     auto inverse = [](uint32_t n) { return (uint32_t)((((uint64_t)1 << 32) + n - 1) / n); };
     const int32_t heads[2] = {Hq, Hk};
     for (int z = 0; z < 2; ++z) {
@@ -498,7 +500,7 @@ gdn_status common(RopeArgs &a, const void *xq, const void *xk, gdn_dtype dt, int
     a.pos = positions; a.inv_freq = inv_freq; a.eps = eps;
     a.rot = rot; a.interleaved = interleaved;
     a.T = T;
-    return T * (int64_t)(Hq + Hk) > ((int64_t)1 << 33) ? GDN_ERR_UNSUPPORTED : GDN_OK;  // the grid's x dimension
+    return GDN_OK;
 }
 
 }  // namespace
@@ -554,8 +556,8 @@ gdn_status gdn_qk_norm_rope_backward(const void *dq, const void *dk, const void 
     if (T > 0 && (!dq || !dxq || (Hk > 0 && (!dk || !dxk)))) return GDN_ERR_INVALID_ARGUMENT;
     const int64_t esz = io_dtype == GDN_DTYPE_BF16 ? 2 : 4;
     if (dxq_stride < (int64_t)Hq * D || (Hk > 0 && dxk_stride < (int64_t)Hk * D)) return GDN_ERR_INVALID_ARGUMENT;
-    if ((dxq_stride * esz) % 16 || (Hk > 0 && (dxk_stride * esz) % 16)) return GDN_ERR_INVALID_ARGUMENT;
     if (dxq_stride > 0x3fffffff || (Hk > 0 && dxk_stride > 0x3fffffff)) return GDN_ERR_UNSUPPORTED;
+    if ((dxq_stride * esz) % 16 || (Hk > 0 && (dxk_stride * esz) % 16)) return GDN_ERR_INVALID_ARGUMENT;
     const void *all[] = {dq, dk, xq, xk, wq, wk, positions, inv_freq, dxq, dxk, dwq, dwk, workspace};
     for (const void *p : all)
         if (p && !gdn::aligned16(p)) return GDN_ERR_INVALID_ARGUMENT;

@@ -541,7 +541,7 @@ GDN_API size_t gdn_prefill_host_scratch_bytes(int64_t T, int32_t Hqk, int32_t Hv
  * decay); it is a constant of the layer, no call gives a gradient for it.
  * scale multiplies the outputs only, never the state.  Sums and states are
  * fp32; bf16 outputs are rounded once.  Dk and Dv in {16, 32, 64, 128}, either
- * dtype; T < 2^31 and (T / 128 + N) * Hv < 2^29, else GDN_ERR_UNSUPPORTED.
+ * dtype; T < 2^31 and (T / 128 + N + 1) * Hv < 2^29, else GDN_ERR_UNSUPPORTED.
  *
  * Kernels: with bf16 I/O, Dk = Dv = 128 and more than 16 tokens a sequence on
  * average (the gradients: 2), chunks of 128 tokens on tensor cores (tcgen05);
@@ -636,7 +636,8 @@ GDN_API size_t gdn_linear_prefill_backward_workspace_bytes(int32_t N, int64_t T,
  * gdn_linear_decode_step -- one token of N sequences, in place on the states:
  * S <- lam S + v k^T, o = scale S q.  Arguments as gdn_decode_step, with
  * log_decay [Hv] and scale in place of g and beta.  Supported: Dk in
- * {16, 32, 64, 128}, any Dv >= 1, either dtype.
+ * {16, 32, 64, 128}, 1 <= Dv <= 2^30, either dtype, N * Hv < 2^31 (where Dk is
+ * 128, that times Dv / 128 rounded up).
  */
 GDN_API gdn_status gdn_linear_decode_step(const void *q, const void *k, const void *v,
                                           gdn_dtype io_dtype, const float *log_decay, float scale,
@@ -684,7 +685,8 @@ GDN_API gdn_status gdn_linear_decode_step_slots(const void *q, const void *k, co
  *                       1: (y[2i], y[2i + 1]).
  *   q, k                outputs [T][Hq][D], [T][Hk][D] io_dtype, contiguous;
  *                       computed in fp32, rounded once.
- * Supported: D in {16, 32, 64, 128, 256}, Hq + Hk <= 32768, either dtype.
+ * Supported: D in {16, 32, 64, 128, 256}, Hq + Hk <= 32768, T * (Hq + Hk) <=
+ * 2^33, either dtype.
  */
 GDN_API gdn_status gdn_qk_norm_rope(const void *xq, const void *xk, gdn_dtype io_dtype,
                                     int64_t xq_stride, int64_t xk_stride, const float *wq,
