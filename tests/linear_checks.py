@@ -43,3 +43,14 @@ def worst_state(x, ref):
     """The largest relative L2 error of x [N,H,Dv,Dk] over (sequence, head)."""
     x, ref = np.asarray(x, dtype=np.float64), np.asarray(ref, dtype=np.float64)
     return float((np.sqrt(((x - ref) ** 2).sum((2, 3))) / np.sqrt((ref ** 2).sum((2, 3)))).max())
+
+
+def dw_bound(dy, n, additions=600):
+    """What a norm weight's gradient, the sum over rows [T,H,D] of dy n in fp32, may be off
+    by, per column.  A term is within 2 (D + 64) u of its row's largest (the turned
+    gradient, the row's inverse root), and passes through at most `additions` partial
+    sums, each rounded by u of what it holds.  Rows are independent, so all of it adds in
+    quadrature; three times that is allowed."""
+    D = dy.shape[-1]
+    size = np.abs(dy).max(-1, keepdims=True) * np.abs(n)
+    return 3 * (2 * (D + 64) + additions) * U * np.sqrt((size ** 2).sum((0, 1)))

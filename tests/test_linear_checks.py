@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import oracle
-from tests.linear_checks import CHUNK, OUT_BOUND, state_bound, worst_chunk, worst_state
+from tests.linear_checks import CHUNK, OUT_BOUND, dw_bound, state_bound, worst_chunk, worst_state
 
 D = 128
 
@@ -86,3 +86,12 @@ def test_a_lost_third_part_of_the_values_is_seen(n, g):
     # sqrt(exp(-1)) 40 u = 24 u is within the bound.  Undecayed, a bf16 value is one part.
     if -0.2 < g < 0:
         assert worst_state(chunked(q, k, v, g, value_parts=2)[1], s_ref) > state_bound(chunks)
+
+
+def test_a_lost_row_of_a_weight_gradient_is_seen():
+    """Of 72,000 rows: one missing row is past the bound in most columns, 128 in nearly all."""
+    rng = np.random.default_rng(8)
+    dy, n = rng.standard_normal((2, 3000, 24, 64))
+    bound = dw_bound(dy, n)
+    one, block = dy[77, 5] * n[77, 5], (dy[40:, 3] * n[40:, 3])[:128].sum(0)
+    assert (np.abs(one) > bound).mean() > 0.7 and (np.abs(block) > bound).mean() > 0.95
