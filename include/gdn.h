@@ -547,9 +547,15 @@ GDN_API size_t gdn_prefill_host_scratch_bytes(int64_t T, int32_t Hqk, int32_t Hv
  * average (the gradients: 2), chunks of 128 tokens on tensor cores (tcgen05);
  * their operands are bf16 (the masked scores and the states entering a chunk are
  * rounded to it, 2^-8 of a term), the fp32 states keep fp32 accuracy.  Everything
- * else runs a token at a time in fp32 on CUDA cores.  A value that is not finite
- * spreads as the sums have it, and on tensor cores also to earlier tokens of its
- * own 128-token chunk and head; never to another sequence.
+ * else runs a token at a time in fp32 on CUDA cores.
+ *
+ * A value that is not finite spreads as the sums have it.  On tensor cores two
+ * things are different.  Where the formula masks a token, the product is 0 times
+ * its value: a NaN or infinity in v also reaches o of the earlier tokens of its own
+ * 128-token chunk (in its head and column), one in dO, q or k the gradients of
+ * the other tokens of its chunk.  And an infinity may arrive as a NaN.  It never
+ * reaches the sums of other heads, chunks on the other side of it, or another
+ * sequence.
  */
 
 /*
