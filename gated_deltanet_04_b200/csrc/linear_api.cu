@@ -75,9 +75,9 @@ size_t prefill_bytes(const Call &c) {
     return seg_bytes(c, gdn::linear::recurrent_seg_len(c.N, c.T, c.Hv, c.Dk, c.Dv));
 }
 
-// Tensor cores: the images of S and of G, and the segment states of each.  Otherwise the three gradients run one after another and
-// share the segment states; dq and dk of v-heads that share a q/k head are
-// summed from fp32 partials.
+// Tensor cores: the images of S and of G, and the segment states of each.
+// Otherwise the three gradients run one after another and share the segment
+// states; dq and dk of v-heads that share a q/k head are summed from fp32 partials.
 size_t backward_bytes(const Call &c) {
     if (check(c) != GDN_OK || check_size(c) != GDN_OK || c.T == 0) return 0;
     if (tensor_cores(c, kLeastBackward))
